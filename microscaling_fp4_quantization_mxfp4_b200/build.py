@@ -12,7 +12,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["api.cu", "quantize.cu", "mse.cu", "gemm.cu", "gemv.cu", "noalloc.cu"]
-HEADERS = ["fp4_device.cuh", "fp4_internal.h"]
+HEADERS = ["fp4_device.cuh", "fp4_internal.h", "gemm_device.cuh"]
 LIB = os.path.join(PKG, "libfp4.so")
 OBJDIR = os.path.join(ROOT, "_build")
 

@@ -44,8 +44,10 @@
 
 #include "fp4_device.cuh"
 #include "fp4_internal.h"
+#include "gemm_device.cuh"
 
 namespace fp4lib {
+using namespace fp4tc;
 namespace {
 
 constexpr int BM = 128;
@@ -54,9 +56,7 @@ constexpr int BK_BYTES = BK / 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSfCols = 48;      // one scale-factor buffer: SFA (<= 16 cols) then SFB (<= 32 cols)
 constexpr uint32_t kSfBufs = 4;       // scale buffers in tensor memory (after the accumulators)
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;   // 4 s per wait
 constexpr int kSmemRing = 220 * 1024;   // operand stages + output staging, below the 227 KB a CTA can have
-constexpr int kEpiStage = 4096;         // one 32-row x 64-column bf16 box, 128B-swizzled
 
 template <int FMT>
 struct FmtTraits {
@@ -86,99 +86,6 @@ struct Cfg {
   static constexpr int kSmemBytes = 1024 /*alignment slack*/ + kStages * kStageBytes + kEpiBytes + kBarrierBytes;
 };
 
-// ------------------------------------------------------------ PTX wrappers --
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0u;
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ uint64_t global_timer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Bounded wait: false when the time limit passes or another role raised abort.
-// try_wait with a suspend-time hint: the warp sleeps in hardware until the
-// phase completes or ~20 us pass, instead of spinning on issue slots.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0u;
-}
-// Critical-path wait (producer, MMA issuer): spin on try_wait, checking the
-// abort flag and the time limit every 1024 polls.
-__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023u) == 0u) {
-      if (*abort_flag != 0) return false;
-      if (global_timer() - t0 > kWaitLimitNs) return false;
-    }
-  }
-}
-// Long waits (epilogue warps): sleep in hardware between polls.
-__device__ __noinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer();
-  for (;;) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    if (*abort_flag != 0) return false;
-    if (global_timer() - t0 > kWaitLimitNs) return false;
-  }
-}
-__device__ __forceinline__ void raise_abort(volatile int* abort_flag, unsigned* error) {
-  *abort_flag = 1;
-  atomicOr(error, 1u);
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_cp_sf(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
 template <int FMT>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                        uint32_t sfb, uint32_t accumulate) {
@@ -196,90 +103,6 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t adesc, uint64_t bdes
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
         : "memory");
   }
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// Waits for this thread's tensor-memory loads into r[4][32].  The registers are in-out operands of
-// the wait (and of an empty statement right after it), so the compiler cannot schedule any use of
-// them ahead of the wait.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[4][32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]), "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[0][8]), "+r"(r[0][9]), "+r"(r[0][10]), "+r"(r[0][11]), "+r"(r[0][12]), "+r"(r[0][13]), "+r"(r[0][14]), "+r"(r[0][15]), "+r"(r[0][16]), "+r"(r[0][17]), "+r"(r[0][18]), "+r"(r[0][19]), "+r"(r[0][20]), "+r"(r[0][21]), "+r"(r[0][22]), "+r"(r[0][23]), "+r"(r[0][24]), "+r"(r[0][25]), "+r"(r[0][26]), "+r"(r[0][27]), "+r"(r[0][28]), "+r"(r[0][29]), "+r"(r[0][30]), "+r"(r[0][31]),
-                 "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]), "+r"(r[1][5]), "+r"(r[1][6]), "+r"(r[1][7]), "+r"(r[1][8]), "+r"(r[1][9]), "+r"(r[1][10]), "+r"(r[1][11]), "+r"(r[1][12]), "+r"(r[1][13]), "+r"(r[1][14]), "+r"(r[1][15]), "+r"(r[1][16]), "+r"(r[1][17]), "+r"(r[1][18]), "+r"(r[1][19]), "+r"(r[1][20]), "+r"(r[1][21]), "+r"(r[1][22]), "+r"(r[1][23]), "+r"(r[1][24]), "+r"(r[1][25]), "+r"(r[1][26]), "+r"(r[1][27]), "+r"(r[1][28]), "+r"(r[1][29]), "+r"(r[1][30]), "+r"(r[1][31])
-               :
-               : "memory");
-  asm volatile(""
-               : "+r"(r[2][0]), "+r"(r[2][1]), "+r"(r[2][2]), "+r"(r[2][3]), "+r"(r[2][4]), "+r"(r[2][5]), "+r"(r[2][6]), "+r"(r[2][7]), "+r"(r[2][8]), "+r"(r[2][9]), "+r"(r[2][10]), "+r"(r[2][11]), "+r"(r[2][12]), "+r"(r[2][13]), "+r"(r[2][14]), "+r"(r[2][15]), "+r"(r[2][16]), "+r"(r[2][17]), "+r"(r[2][18]), "+r"(r[2][19]), "+r"(r[2][20]), "+r"(r[2][21]), "+r"(r[2][22]), "+r"(r[2][23]), "+r"(r[2][24]), "+r"(r[2][25]), "+r"(r[2][26]), "+r"(r[2][27]), "+r"(r[2][28]), "+r"(r[2][29]), "+r"(r[2][30]), "+r"(r[2][31]),
-                 "+r"(r[3][0]), "+r"(r[3][1]), "+r"(r[3][2]), "+r"(r[3][3]), "+r"(r[3][4]), "+r"(r[3][5]), "+r"(r[3][6]), "+r"(r[3][7]), "+r"(r[3][8]), "+r"(r[3][9]), "+r"(r[3][10]), "+r"(r[3][11]), "+r"(r[3][12]), "+r"(r[3][13]), "+r"(r[3][14]), "+r"(r[3][15]), "+r"(r[3][16]), "+r"(r[3][17]), "+r"(r[3][18]), "+r"(r[3][19]), "+r"(r[3][20]), "+r"(r[3][21]), "+r"(r[3][22]), "+r"(r[3][23]), "+r"(r[3][24]), "+r"(r[3][25]), "+r"(r[3][26]), "+r"(r[3][27]), "+r"(r[3][28]), "+r"(r[3][29]), "+r"(r[3][30]), "+r"(r[3][31]));
-}
-
-// Shared-memory matrix descriptor: K-major operand, 128-byte rows, 128B
-// swizzle, 8-row groups 1024 bytes apart (Blackwell descriptor version 1).
-// TMA store of one box from shared memory, and bulk-group completion.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(x), "r"(y)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// One epilogue warp's 32 rows x 128 accumulator columns (r[c][i] = column 32c + i of row
-// y0 + lane) -> alpha * value in bf16 -> two 32 x 64 boxes through the warp's 4 KB staging
-// buffer (1024-byte aligned, 128B-swizzled: 16-byte chunk j of row i at chunk j ^ (i & 7), the
-// layout the tensor map's SWIZZLE_128B expects) -> TMA stores, which clip rows >= M and columns
-// >= N.  The buffer is reused for the second box once the first store has read it.
-__device__ __forceinline__ void epi_store_bf16_tma(const CUtensorMap* tmap_y, uint8_t* stg, const uint32_t (&r)[4][32],
-                                                   float alpha, int x0, int y0, int M, int N, int lane) {
-  const uint32_t base = smem_u32(stg) + (uint32_t)lane * 128u;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (lane == 0) bulk_wait_read0();        // the previous box's store has read the buffer
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = __fmul_rn(__uint_as_float(r[2 * h + (j >> 2)][(j & 3) * 8 + 2 * i]), alpha);
-        const float hi = __fmul_rn(__uint_as_float(r[2 * h + (j >> 2)][(j & 3) * 8 + 2 * i + 1]), alpha);
-        w[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(lo)) |
-               ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(hi)) << 16);
-      }
-      const uint32_t dst = base + (uint32_t)(((j ^ (lane & 7)) & 7) * 16);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                   : "memory");
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> async-proxy reads
-    __syncwarp();
-    if (lane == 0 && x0 + 64 * h < N && y0 < M) {       // boxes wholly past the edge are skipped
-      tma_store_2d(tmap_y, smem_u32(stg), x0 + 64 * h, y0);
-      bulk_commit_group();
-    }
-  }
-}
-
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
-}
-// Descriptor of one 512-byte scale atom: 32 rows of 16 bytes, no swizzle,
-// 8-row core matrices 128 bytes apart.
-__device__ __forceinline__ uint64_t desc_sf(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(128u >> 4) << 32) |
-         ((uint64_t)1u << 46);
 }
 
 // Instruction descriptor of the block-scaled MMA: E2M1 x E2M1, K-major
@@ -312,13 +135,6 @@ struct KernelArgs {
   uint32_t q_mx_thr;
   fp4dev::PhiloxKeys q_keys;
 };
-
-// One 32-byte store (a whole L2 sector) of eight 32-bit words; dst 32-byte aligned.
-__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 
 // Byte offset of the scale of (row m, group g) of the quantized Y.
 __device__ __forceinline__ long long q_sf_offset(const KernelArgs& p, int m, int g, int groups) {
@@ -382,16 +198,6 @@ __device__ __forceinline__ void epi_quantize32(const KernelArgs& p, uint32_t (&r
     }
   }
   *reinterpret_cast<uint4*>(p.q_codes + (size_t)m * (unsigned)(p.N / 2) + n0 / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int& mt, int& nt) {
-  constexpr int kGroup = 8;
-  const int band = t / (kGroup * num_n);
-  const int first = band * kGroup;
-  const int gsize = min(kGroup, num_m - first);
-  const int local = t - band * kGroup * num_n;
-  mt = first + local % gsize;
-  nt = local / gsize;
 }
 
 template <int BN, int FMT, bool BF16, int QO = 0>
@@ -791,43 +597,6 @@ struct Cfg2 {
   static_assert(kSfBase + kSfBufs * kSfCols <= kTmemCols, "tensor memory budget");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// shared::cluster address of the same shared-memory location in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t d;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
-  return d;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-// commit of the pair's tensor-core work to a barrier of this CTA only
-__device__ __forceinline__ void tc_commit_pair_local(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_cp_sf_pair(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
 template <int FMT>
 __device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                             uint32_t sfb, uint32_t accumulate) {
@@ -1191,15 +960,6 @@ struct Part {
   static constexpr int kBytes = 128 * kStride * 4;
 };
 
-// Called only between the two cluster barriers, which order it against the partials' stores.
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
-
 template <int BN, int FMT, bool BF16>
 __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
     fp4_gemm_splitk_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -1228,7 +988,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = pair::cluster_rank();
+  const uint32_t rank = cluster_rank();
   const int tile = (int)(blockIdx.x / (uint32_t)split);
   int mt, nt;
   tile_coords(tile, p.num_m, p.num_n, mt, nt);
@@ -1420,7 +1180,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
   (void)have_part;
   tc_fence_before();
   __syncthreads();
-  pair::cluster_sync_all();                 // every CTA's partial tile is in its shared memory
+  cluster_sync_all();                 // every CTA's partial tile is in its shared memory
 
   // ------------------------------------------- reduce one slice across ranks --
   {
@@ -1436,7 +1196,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
       float4 v[kMaxSplit];                                       // all remote loads in flight at once
 #pragma unroll
       for (int s = 0; s < kMaxSplit; ++s)
-        if (s < split) v[s] = ld_cluster_f4(pair::map_rank(addr, (uint32_t)s));
+        if (s < split) v[s] = ld_cluster_f4(map_rank(addr, (uint32_t)s));
       float4 acc = v[0];
 #pragma unroll
       for (int s = 1; s < kMaxSplit; ++s)
@@ -1473,7 +1233,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
       }
     }
   }
-  pair::cluster_sync_all();                 // no CTA leaves while a peer may still read its partial
+  cluster_sync_all();                 // no CTA leaves while a peer may still read its partial
   tc_fence_after();
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -1520,14 +1280,6 @@ struct CfgS {
   static_assert(BNT == 16 || BNT == 32 || BNT == 64 || BNT == 128, "activation tile");
 };
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
 template <int BNT, int FMT, bool BF16>
 __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
     fp4_gemm_swap_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -1555,7 +1307,7 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = split > 1 ? pair::cluster_rank() : 0u;
+  const uint32_t rank = split > 1 ? cluster_rank() : 0u;
   const int nt = (int)(blockIdx.x / (uint32_t)split);           // 128-row weight tile
   const int nkb = (p.K + BK - 1) / BK;
   const int kb0 = (int)((int64_t)nkb * rank / split), kb1 = (int)((int64_t)nkb * (rank + 1) / split);
@@ -1751,7 +1503,7 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (split > 1) pair::cluster_sync_all();  // every CTA's partial tile is in its shared memory
+  if (split > 1) cluster_sync_all();  // every CTA's partial tile is in its shared memory
 
   // ------------------------------------------- reduce one slice across ranks --
   {
@@ -1770,7 +1522,7 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
       } else {
 #pragma unroll
         for (int s = 0; s < splitk::kMaxSplit; ++s)
-          if (s < split) v[s] = splitk::ld_cluster_f4(pair::map_rank(addr, (uint32_t)s));
+          if (s < split) v[s] = ld_cluster_f4(map_rank(addr, (uint32_t)s));
       }
       float4 acc = v[0];
 #pragma unroll
@@ -1807,7 +1559,7 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
       }
     }
   }
-  if (split > 1) pair::cluster_sync_all();  // no CTA leaves while a peer may still read its partial
+  if (split > 1) cluster_sync_all();  // no CTA leaves while a peer may still read its partial
   tc_fence_after();
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -1818,20 +1570,6 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
 
 
 // ------------------------------------------------------------------ host ---
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode;
-}
-
 // 2-D uint8 view [rows, K/2] of packed codes, box 128 bytes x box_rows, 128B swizzle.
 bool make_code_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t kbytes, int box_rows) {
   auto enc = encode_fn();
