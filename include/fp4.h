@@ -55,6 +55,20 @@
  *    are (rows, cols) for axis 1 and (cols, rows) for axis 0.
  *
  * Supported (format, block): (FP4_MXFP4, 32), (FP4_NVFP4, 16).
+ *
+ * 8-bit operators (fp4_fp8_*, fp4_rmsnorm_*), for the layers and gradients that four bits are too few
+ * for:
+ *  - Codes: one byte an element, E4M3 (largest value 448) or E5M2 (57344), rows `ldc` bytes apart
+ *    (ldc >= L, a multiple of 16; the bytes past L in a row are neither read nor written).
+ *  - Scales: one E8M0 byte b (2^(b-127)) per block of 128 elements along the row (the last block may be
+ *    shorter) or per 128 x 128 tile, whose byte then stands in each of its rows.  The exponent is the
+ *    least E >= -127 with amax <= Fmax * 2^E, so that no element saturates; byte 0 for an all-zero
+ *    block.  A block that holds an infinity or a NaN gets byte 255 and NaN codes.
+ *  - Scale layouts as above with ceil(L / 128) groups a row; the product reads FP4_SF_MMA.
+ *  - Codes are rounded to nearest, ties to even, once: x * 2^-E is exact.
+ *  - These calls allocate nothing beyond the library's per-device scratch, share no buffer that holds
+ *    results, and may run on several streams at once.  They may be captured into a CUDA graph once the
+ *    library has been used on the device outside a capture.
  */
 #ifndef FP4_H_
 #define FP4_H_
@@ -334,6 +348,94 @@ fp4_status fp4_amax_noalloc(const void* x, int64_t rows, int64_t cols, int64_t l
 /* fp4_nv_tensor_scale -- s_t = fp32(amax / 2688), 1.0 for amax == 0, on the
  * device (one thread).  amax and tensor_scale_out are device fp32 pointers. */
 fp4_status fp4_nv_tensor_scale(const float* amax, float* tensor_scale_out, void* stream);
+
+/* Codes of the 8-bit operators. */
+enum { FP4_E4M3 = 0, FP4_E5M2 = 1 };                /* fp4_fp8_format */
+
+/*
+ * fp4_fp8_quantize -- block-scaled FP8 quantization of a bf16 matrix, 128 elements a block.
+ *   x          bf16 [rows, cols], row stride ld; 16-byte aligned; cols and ld multiples of 8.
+ *   fmt        FP4_E4M3 or FP4_E5M2.
+ *   axis       1: blocks along cols (out_rows = rows, L = cols); 0: blocks along rows, output transposed
+ *              (out_rows = cols, L = rows).  L need not be a multiple of 128.
+ *   codes      uint8 [out_rows, L], row stride ldc; 16-byte aligned.
+ *   scales     fp4_fp8_scales_bytes(rows, cols, axis, sf_layout) bytes; 4-byte aligned for FP4_SF_MMA.
+ */
+fp4_status fp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int fmt, int axis,
+                            uint8_t* codes, int64_t ldc, uint8_t* scales, int sf_layout, void* stream);
+
+/*
+ * fp4_fp8_quantize_2d -- one scale per 128 x 128 tile (weights): W along its rows and, with the same
+ * codes, W^T along its rows, so that the forward product and the data gradient's see one W.
+ *   codes, scales      as fp4_fp8_quantize axis 1.
+ *   codes_t, scales_t  as fp4_fp8_quantize axis 0; both null to skip, or both given.
+ */
+fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_t ld, int fmt,
+                               uint8_t* codes, int64_t ldc, uint8_t* scales, uint8_t* codes_t, int64_t ldc_t,
+                               uint8_t* scales_t, int sf_layout, void* stream);
+
+/*
+ * fp4_fp8_dequantize -- codes [rows, cols] (row stride ldc) and scales back to fp32 or bf16
+ * [rows, cols], row stride cols, 16-byte aligned: code * 2^(b-127) in fp32, NaN for b = 255.
+ */
+fp4_status fp4_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,
+                              int fmt, int sf_layout, void* out, int out_dtype, void* stream);
+
+/*
+ * fp4_fp8_gemm -- block-scaled FP8 x FP8 product with fp32 accumulation on the tcgen05 tensor cores:
+ *   Y[M,N] = sum_k a[m,k] b[n,k], each element its code times its block's scale.
+ *   a, b       codes [M, K] and [N, K], row strides lda and ldb; a_fmt and b_fmt FP4_E4M3 or FP4_E5M2,
+ *              independently.  16-byte aligned.
+ *   a_sf, b_sf scales in FP4_SF_MMA layout, 16-byte aligned.
+ *   y          fp32 or bf16 [M, N], row stride ldy >= N; aligned to its element.
+ * M, N, K >= 1 arbitrary.  Forward: x and W; data gradient: dY and W^T of fp4_fp8_quantize_2d; weight
+ * gradient: dY and x both quantized along the tokens (axis 0).
+ */
+fp4_status fp4_fp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_sf, const uint8_t* b, int64_t ldb,
+                        const uint8_t* b_sf, int64_t M, int64_t N, int64_t K, int a_fmt, int b_fmt, void* y,
+                        int64_t ldy, int y_dtype, void* stream);
+
+/*
+ * fp4_rmsnorm_fp8_quantize -- residual addition, RMS norm and FP8 quantization in one pass:
+ *   h = bf16(x + residual), or x without one;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * weight in
+ *   fp32, quantized along the row as fp4_fp8_quantize does (axis 1).
+ *   x, residual    bf16 [rows, cols], row strides ldx and ldr (multiples of 8); residual nullable.
+ *   weight         [cols], bf16 or fp32 (weight_dtype FP4_OUT_BF16 or FP4_OUT_F32).
+ *   cols           a multiple of 8, at most 16384.
+ *   eps            >= 0, finite.
+ *   residual_out   bf16 [rows, cols] contiguous: h (may be x's or residual's own memory, with the same
+ *                  row stride); required with a residual, null without one.
+ *   rstd           nullable fp32 [rows]; norm_out nullable bf16 [rows, cols] contiguous: y (what the
+ *                  weight gradient quantizes along the tokens).
+ * x, residual, weight, residual_out and norm_out 16-byte aligned.
+ */
+fp4_status fp4_rmsnorm_fp8_quantize(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                    int weight_dtype, int64_t rows, int64_t cols, float eps, int fmt, uint8_t* codes,
+                                    int64_t ldc, uint8_t* scales, int sf_layout, void* residual_out, float* rstd,
+                                    void* norm_out, void* stream);
+
+/*
+ * fp4_rmsnorm_backward -- gradients of y = h * rstd * weight (rstd a function of h):
+ *   g = dy * weight, xh = h * rstd;  dx = rstd * (g - xh * mean(g * xh)) + dresidual;
+ *   dweight = sum over rows of dy * xh, in a fixed order (two calls give the same bits).
+ *   dy, h, dresidual  bf16 [rows, cols], row strides lddy, ldh, lddr (multiples of 8); dresidual, the
+ *                     gradient that reaches h past the norm, nullable.  dx is the gradient of both x and
+ *                     residual.
+ *   weight, cols      as fp4_rmsnorm_fp8_quantize; rstd fp32 [rows] from it.
+ *   dx                bf16 [rows, cols] contiguous (may be dy's, h's or dresidual's own memory, with the
+ *                     same row stride); dweight fp32 [cols].
+ *   workspace         fp4_rmsnorm_backward_workspace(rows, cols) bytes, the call's own while it runs.
+ * All but rstd 16-byte aligned.
+ */
+fp4_status fp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                                int weight_dtype, const float* rstd, const void* dresidual, int64_t lddr, int64_t rows,
+                                int64_t cols, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                                void* stream);
+/* Workspace bytes of fp4_rmsnorm_backward on the current device; 0 on bad arguments. */
+size_t fp4_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+
+/* Bytes of scales of the 8-bit operators for a [rows, cols] input quantized along `axis`; 0 on bad arguments. */
+size_t fp4_fp8_scales_bytes(int64_t rows, int64_t cols, int axis, int sf_layout);
 
 /* Bytes of packed codes for a [rows, cols] input (either axis). */
 size_t fp4_codes_bytes(int64_t rows, int64_t cols);

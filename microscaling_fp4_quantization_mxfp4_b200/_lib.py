@@ -7,6 +7,7 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp4.so")
 
 _i64, _u64, _int, _vp, _sz = ctypes.c_int64, ctypes.c_uint64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/fp4.h
 PROTOTYPES = {
@@ -24,6 +25,16 @@ PROTOTYPES = {
     "fp4_gemm": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _i64, _int, _vp]),
     "fp4_gemm_quantize": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _int, _int, _int, _u64,
                                  _vp, _vp, _vp, _int, _vp]),
+    "fp4_fp8_quantize": (_int, [_vp, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp, _int, _vp]),
+    "fp4_fp8_quantize_2d": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _i64, _vp, _int, _vp]),
+    "fp4_fp8_dequantize": (_int, [_vp, _i64, _vp, _i64, _i64, _int, _int, _vp, _int, _vp]),
+    "fp4_fp8_gemm": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _int, _int, _vp, _i64, _int, _vp]),
+    "fp4_rmsnorm_fp8_quantize": (_int, [_vp, _i64, _vp, _i64, _vp, _int, _i64, _i64, _f32, _int, _vp, _i64, _vp, _int,
+                                        _vp, _vp, _vp, _vp]),
+    "fp4_rmsnorm_backward": (_int, [_vp, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _sz,
+                                    _vp]),
+    "fp4_rmsnorm_backward_workspace": (_sz, [_i64, _i64]),
+    "fp4_fp8_scales_bytes": (_sz, [_i64, _i64, _int, _int]),
     "fp4_amax": (_int, [_vp, _i64, _i64, _i64, _vp, _vp]),
     "fp4_amax_noalloc": (_int, [_vp, _i64, _i64, _i64, _vp, _vp]),
     "fp4_nv_tensor_scale": (_int, [_vp, _vp, _vp]),

@@ -8,6 +8,7 @@ every call raises if libfp4.so is missing or a tensor is not on a GPU.
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -25,6 +26,10 @@ _RND = {"rtn": RTN, "sr": SR, RTN: RTN, SR: SR}
 _SF = {"rowmajor": SF_ROWMAJOR, "mma": SF_MMA, SF_ROWMAJOR: SF_ROWMAJOR, SF_MMA: SF_MMA}
 _OUT = {"f32": OUT_F32, "bf16": OUT_BF16, torch.float32: OUT_F32, torch.bfloat16: OUT_BF16,
         OUT_F32: OUT_F32, OUT_BF16: OUT_BF16}
+E4M3, E5M2 = 0, 1
+_FMT8 = {"e4m3": E4M3, "e5m2": E5M2, torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2, E4M3: E4M3, E5M2: E5M2}
+_BYTE = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu)
+FP8_BLOCK = 128
 BLOCK = {MXFP4: 32, NVFP4: 16, NVFP4_4O6: 16, MXFP4_GS: 32}
 
 
@@ -39,6 +44,18 @@ class Fp4Quantized(NamedTuple):
     codes: torch.Tensor          # uint8 [out_rows, L/2]
     scales: torch.Tensor         # uint8, row-major [out_rows, L/block] or flat tensor-core layout
     tensor_scale: Optional[torch.Tensor]   # fp32 [1] (NVFP4) or None
+
+
+class Fp8Quantized(NamedTuple):
+    codes: torch.Tensor          # uint8 [out_rows, L], rows a multiple of 16 bytes apart
+    scales: torch.Tensor         # uint8, row-major [out_rows, ceil(L / 128)] or flat tensor-core layout
+
+
+class Fp8RmsNorm(NamedTuple):
+    codes: torch.Tensor                    # as Fp8Quantized
+    scales: torch.Tensor
+    residual_out: Optional[torch.Tensor]   # bf16 x + residual, or None without a residual
+    rstd: torch.Tensor                     # fp32 [rows]
 
 
 def _check(status: int, where: str) -> None:
@@ -280,3 +297,235 @@ def fp4_nv_tensor_scale(amax: torch.Tensor, *, out=None, stream=None) -> torch.T
     _check(_lib.load().fp4_nv_tensor_scale(amax.data_ptr(), out.data_ptr(), _stream(stream)),
            "fp4_nv_tensor_scale")
     return out
+
+
+# ------------------------------------------------------------ 8-bit operators ---
+def _where_it_lives(fn):
+    """Run `fn` with its first tensor's device current and, if given, on `stream`: outputs and workspaces
+    are then allocated for the stream that uses them."""
+    @functools.wraps(fn)
+    def call(x, *args, stream=None, **kwargs):
+        _need_cuda(x, "the first argument")
+        if stream is None and x.get_device() == torch._C._cuda_getDevice():
+            return fn(x, *args, **kwargs)
+        if stream is not None and stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+        with torch.cuda.device(x.device), torch.cuda.stream(stream):
+            return fn(x, *args, **kwargs)
+    return call
+
+
+def _same_device(x: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, the first argument on {x.device}")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor with unit column stride (a single row's own stride says nothing)."""
+    return t.stride(0) if t.shape[0] != 1 else t.shape[1]
+
+
+def _bf16_rows(x: torch.Tensor, shape, name: str) -> int:
+    if x.dtype != torch.bfloat16 or x.shape != shape or x.stride(1) != 1:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} with unit column stride")
+    return _row_stride(x)
+
+
+def _contiguous(t: torch.Tensor, shape, dtype, name: str) -> torch.Tensor:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _pitch(t: torch.Tensor) -> int:
+    """Row stride of 8-bit codes (a single row: its length rounded up to 16)."""
+    return t.stride(0) if t.shape[0] != 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _codes8(t: torch.Tensor, name: str, shape=None) -> int:
+    if t.dtype not in _BYTE or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1) or \
+            (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be 8-bit codes" + (f" of shape {tuple(shape)}" if shape is not None else
+                                                          ", 2-D") + " with unit column stride")
+    return _pitch(t)
+
+
+def _scales_shape(rows: int, length: int, sf: int):
+    g = (length + FP8_BLOCK - 1) // FP8_BLOCK
+    return (rows, g) if sf == SF_ROWMAJOR else ((rows + 127) // 128 * 128 * ((g + 3) // 4 * 4),)
+
+
+def _scales8(t: torch.Tensor, rows: int, length: int, sf: int, name: str) -> None:
+    shape = _scales_shape(rows, length, sf)
+    if t.dtype not in _BYTE or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous scale bytes of shape {tuple(shape)}")
+
+
+def _fp8_outputs(x, rows, length, sf, codes, scales, name=""):
+    """Checked or new codes [rows, length] and scales; returns (codes, row stride, scales)."""
+    if codes is None:
+        pitch = (length + 15) // 16 * 16
+        codes = torch.empty((rows, pitch), dtype=torch.uint8, device=x.device)
+        if pitch != length:
+            codes = codes[:, :length]
+    else:
+        _same_device(x, **{"codes" + name: codes})
+        pitch = _codes8(codes, "codes" + name, (rows, length))
+    if scales is None:
+        scales = torch.empty(_scales_shape(rows, length, sf), dtype=torch.uint8, device=x.device)
+    else:
+        _same_device(x, **{"scales" + name: scales})
+        _scales8(scales, rows, length, sf, "scales" + name)
+    return codes, pitch, scales
+
+
+def fp4_fp8_scales_bytes(rows: int, cols: int, axis: int, sf_layout="rowmajor") -> int:
+    """Bytes of 8-bit block scales (128 elements a block) for a [rows, cols] tensor quantized along `axis`;
+    0 for an invalid shape."""
+    return _lib.load().fp4_fp8_scales_bytes(rows, cols, axis, _SF[sf_layout])
+
+
+@_where_it_lives
+def fp4_fp8_quantize(x: torch.Tensor, fmt="e4m3", axis: int = 1, sf_layout="rowmajor", *, codes=None,
+                     scales=None) -> Fp8Quantized:
+    """bf16 [rows, cols] -> E4M3 or E5M2 codes with one power-of-two scale per 128 elements along `axis` (0: of
+    the transpose); see fp4_fp8_quantize in include/fp4.h.  `stream=` runs it on that stream."""
+    _bf16_matrix(x)
+    f, sf = _FMT8[fmt], _SF[sf_layout]
+    rows, cols = x.shape
+    orows, length = (rows, cols) if axis == 1 else (cols, rows)
+    codes, pitch, scales = _fp8_outputs(x, orows, length, sf, codes, scales)
+    _check(_lib.load().fp4_fp8_quantize(x.data_ptr(), rows, cols, _row_stride(x), f, axis, codes.data_ptr(), pitch,
+                                        scales.data_ptr(), sf, _stream(None)), "fp4_fp8_quantize")
+    return Fp8Quantized(codes, scales)
+
+
+@_where_it_lives
+def fp4_fp8_quantize_2d(x: torch.Tensor, fmt="e4m3", sf_layout="rowmajor", transposed: bool = True, *, codes=None,
+                        scales=None, codes_t=None, scales_t=None):
+    """One scale per 128 x 128 tile of a bf16 matrix (see fp4_fp8_quantize_2d in include/fp4.h).  Returns
+    (W along its rows, W^T along its rows or None) as Fp8Quantized, with the same codes."""
+    _bf16_matrix(x)
+    f, sf = _FMT8[fmt], _SF[sf_layout]
+    rows, cols = x.shape
+    codes, pitch, scales = _fp8_outputs(x, rows, cols, sf, codes, scales)
+    pitch_t = 0
+    if transposed:
+        codes_t, pitch_t, scales_t = _fp8_outputs(x, cols, rows, sf, codes_t, scales_t, "_t")
+    else:
+        codes_t = scales_t = None
+    _check(_lib.load().fp4_fp8_quantize_2d(x.data_ptr(), rows, cols, _row_stride(x), f, codes.data_ptr(), pitch,
+                                           scales.data_ptr(), _ptr(codes_t), pitch_t, _ptr(scales_t), sf,
+                                           _stream(None)), "fp4_fp8_quantize_2d")
+    return Fp8Quantized(codes, scales), (Fp8Quantized(codes_t, scales_t) if transposed else None)
+
+
+@_where_it_lives
+def fp4_fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt="e4m3", sf_layout="rowmajor", out_dtype="f32", *,
+                       out=None) -> torch.Tensor:
+    """8-bit codes and scales back to fp32 or bf16 [rows, L]."""
+    f, sf, od = _FMT8[fmt], _SF[sf_layout], _OUT[out_dtype]
+    pitch = _codes8(codes, "codes")
+    rows, cols = codes.shape
+    _same_device(codes, scales=scales, out=out)
+    _scales8(scales, rows, cols, sf, "scales")
+    dtype = torch.float32 if od == OUT_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    else:
+        _contiguous(out, (rows, cols), dtype, "out")
+    _check(_lib.load().fp4_fp8_dequantize(codes.data_ptr(), pitch, scales.data_ptr(), rows, cols, f, sf, out.data_ptr(),
+                                          od, _stream(None)), "fp4_fp8_dequantize")
+    return out
+
+
+@_where_it_lives
+def fp4_fp8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
+                 a_fmt="e4m3", b_fmt="e4m3", out_dtype="bf16", *, out=None) -> torch.Tensor:
+    """Y[M, N] = A . B^T of block-scaled 8-bit operands [M, K] and [N, K] on the tensor cores (see fp4_fp8_gemm in
+    include/fp4.h); scales in the tensor-core ("mma") layout.  With `out`, its dtype decides."""
+    af, bf = _FMT8[a_fmt], _FMT8[b_fmt]
+    lda, ldb = _codes8(a_codes, "a_codes"), _codes8(b_codes, "b_codes")
+    M, K = a_codes.shape
+    N = b_codes.shape[0]
+    if b_codes.shape[1] != K:
+        raise ValueError("A and B must have the same K")
+    _same_device(a_codes, a_scales=a_scales, b_codes=b_codes, b_scales=b_scales, out=out)
+    _scales8(a_scales, M, K, SF_MMA, "a_scales")
+    _scales8(b_scales, N, K, SF_MMA, "b_scales")
+    if out is None:
+        od = _OUT[out_dtype]
+        out = torch.empty((M, N), dtype=torch.float32 if od == OUT_F32 else torch.bfloat16, device=a_codes.device)
+    elif out.dtype not in (torch.float32, torch.bfloat16) or out.shape != (M, N) or (out.stride(1) != 1 and N != 1):
+        raise ValueError(f"out must be a bf16 or fp32 tensor of shape {(M, N)} with unit column stride")
+    _check(_lib.load().fp4_fp8_gemm(a_codes.data_ptr(), lda, a_scales.data_ptr(), b_codes.data_ptr(), ldb,
+                                    b_scales.data_ptr(), M, N, K, af, bf, out.data_ptr(), _row_stride(out),
+                                    _OUT[out.dtype], _stream(None)), "fp4_fp8_gemm")
+    return out
+
+
+def _norm_weight(weight: torch.Tensor, cols: int) -> int:
+    if weight.dtype not in (torch.bfloat16, torch.float32) or weight.shape != (cols,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bf16 or fp32 tensor of shape ({cols},)")
+    return _OUT[weight.dtype]
+
+
+@_where_it_lives
+def fp4_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                             eps: float = 1e-6, fmt="e4m3", sf_layout="rowmajor", *, codes=None, scales=None,
+                             residual_out=None, rstd=None, norm_out=None) -> Fp8RmsNorm:
+    """h = x + residual (bf16), y = h / sqrt(mean(h^2) + eps) * weight along the rows, y in 8-bit codes and scales,
+    in one pass (see fp4_rmsnorm_fp8_quantize in include/fp4.h).  norm_out: a bf16 [rows, cols] tensor that
+    receives y as well."""
+    _bf16_matrix(x)
+    f, sf = _FMT8[fmt], _SF[sf_layout]
+    rows, cols = shape = x.shape
+    _same_device(x, weight=weight, residual=residual, residual_out=residual_out, rstd=rstd, norm_out=norm_out)
+    wd = _norm_weight(weight, cols)
+    ldr = 0
+    if residual is not None:
+        ldr = _bf16_rows(residual, shape, "residual")
+        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device) if residual_out is None else \
+            _contiguous(residual_out, shape, torch.bfloat16, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out is given without a residual")
+    rstd = torch.empty((rows,), dtype=torch.float32, device=x.device) if rstd is None else \
+        _contiguous(rstd, (rows,), torch.float32, "rstd")
+    if norm_out is not None:
+        _contiguous(norm_out, shape, torch.bfloat16, "norm_out")
+    codes, pitch, scales = _fp8_outputs(x, rows, cols, sf, codes, scales)
+    _check(_lib.load().fp4_rmsnorm_fp8_quantize(
+        x.data_ptr(), _row_stride(x), _ptr(residual), ldr, weight.data_ptr(), wd, rows, cols, eps, f, codes.data_ptr(),
+        pitch, scales.data_ptr(), sf, _ptr(residual_out), rstd.data_ptr(), _ptr(norm_out), _stream(None)),
+        "fp4_rmsnorm_fp8_quantize")
+    return Fp8RmsNorm(codes, scales, residual_out, rstd)
+
+
+@_where_it_lives
+def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                         dresidual: Optional[torch.Tensor] = None, *, dx=None, dweight=None, workspace=None):
+    """Gradients of y = h * rstd * weight: (dx, the bf16 gradient of h -- of x and of residual alike -- plus
+    `dresidual` where given, dweight in fp32).  See fp4_rmsnorm_backward in include/fp4.h."""
+    _bf16_matrix(dy, "dy")
+    rows, cols = shape = dy.shape
+    _same_device(dy, h=h, weight=weight, rstd=rstd, dresidual=dresidual, dx=dx, dweight=dweight, workspace=workspace)
+    ldh, wd = _bf16_rows(h, shape, "h"), _norm_weight(weight, cols)
+    _contiguous(rstd, (rows,), torch.float32, "rstd")
+    lddr = 0 if dresidual is None else _bf16_rows(dresidual, shape, "dresidual")
+    dx = torch.empty(shape, dtype=torch.bfloat16, device=dy.device) if dx is None else \
+        _contiguous(dx, shape, torch.bfloat16, "dx")
+    dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device) if dweight is None else \
+        _contiguous(dweight, (cols,), torch.float32, "dweight")
+    lib = _lib.load()
+    if workspace is None:
+        # an invalid shape needs 0 bytes: the call below refuses it
+        workspace = torch.empty((max(lib.fp4_rmsnorm_backward_workspace(rows, cols), 16),), dtype=torch.uint8,
+                                device=dy.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check(lib.fp4_rmsnorm_backward(
+        dy.data_ptr(), _row_stride(dy), h.data_ptr(), ldh, weight.data_ptr(), wd, rstd.data_ptr(), _ptr(dresidual), lddr,
+        rows, cols, dx.data_ptr(), dweight.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(None)), "fp4_rmsnorm_backward")
+    return dx, dweight

@@ -8,16 +8,19 @@
 #include <stdio.h>
 #include <stdlib.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "../../include/fp4.h"
 #include "fp4_internal.h"
+#include "fp8_internal.h"
 
 using namespace fp4lib;
 
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxTileRows = 65532;      // row tiles of 128: the grid's second dimension
 
 struct DeviceState {
   bool ready = false;
@@ -188,6 +191,44 @@ fp4_status quantize_impl(const void* x, int64_t rows, int64_t cols, int64_t ld, 
   p.ts = ts_read;
   p.ts_copy_out = ts_copy;
   return from_cuda(launch_quantize(p, d->num_sms, st));
+}
+
+// Checks of the 8-bit operators.
+bool fp8_format(int fmt) { return fmt == FP4_E4M3 || fmt == FP4_E5M2; }
+bool sf_layout_ok(int sf_layout) { return sf_layout == FP4_SF_ROWMAJOR || sf_layout == FP4_SF_MMA; }
+// A bf16 matrix that kernels read in 16-byte chunks.
+fp4_status check_rows16(const void* x, int64_t cols, int64_t ld) {
+  if (x == nullptr || ld < cols) return FP4_ERR_ARG;
+  if (ld % 8 != 0) return FP4_ERR_SHAPE;
+  return aligned16(x) ? FP4_OK : FP4_ERR_ALIGN;
+}
+// Codes [*, len] in rows of ldc bytes.
+fp4_status check_codes(const void* codes, int64_t len, int64_t ldc) {
+  if (codes == nullptr || ldc < len) return FP4_ERR_ARG;
+  return ldc % 16 == 0 && aligned16(codes) ? FP4_OK : FP4_ERR_ALIGN;
+}
+// Scales: the tensor-core layout's padding is written a word at a time.
+fp4_status check_scales(const void* scales, int sf_layout) {
+  if (scales == nullptr || !sf_layout_ok(sf_layout)) return FP4_ERR_ARG;
+  return sf_layout == FP4_SF_MMA && (reinterpret_cast<uintptr_t>(scales) & 3u) != 0 ? FP4_ERR_ALIGN : FP4_OK;
+}
+fp4_status check_norm_shape(int64_t rows, int64_t cols, const void* weight, int weight_dtype) {
+  if (rows <= 0 || cols <= 0 || weight == nullptr) return FP4_ERR_ARG;
+  if (weight_dtype != FP4_OUT_F32 && weight_dtype != FP4_OUT_BF16) return FP4_ERR_ARG;
+  if (cols % 8 != 0 || cols > kMaxNormCols || rows >= (int64_t)1 << 31) return FP4_ERR_SHAPE;
+  return aligned16(weight) ? FP4_OK : FP4_ERR_ALIGN;
+}
+// SMs of the current device, without the scratch that device_state allocates.
+fp4_status device_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FP4_ERR_CUDA;
+  static std::atomic<int> known[kMaxDevices];
+  *sms = known[dev].load(std::memory_order_relaxed);
+  if (*sms == 0) {
+    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return FP4_ERR_CUDA;
+    known[dev].store(*sms, std::memory_order_relaxed);
+  }
+  return FP4_OK;
 }
 
 }  // namespace
@@ -445,6 +486,200 @@ fp4_status fp4_gemm_quantize(const uint8_t* a, const uint8_t* a_sf, const float*
   cudaError_t e = launch_gemm(p, d->num_sms, st);
   if (e == cudaErrorNotSupported) return FP4_ERR_UNSUPPORTED;
   return from_cuda(e);
+}
+
+fp4_status fp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int fmt, int axis, uint8_t* codes,
+                            int64_t ldc, uint8_t* scales, int sf_layout, void* stream) {
+  fp4_status s = check_input(x, rows, cols, ld);
+  if (s != FP4_OK) return s;
+  if (!fp8_format(fmt) || (axis != 0 && axis != 1)) return FP4_ERR_ARG;
+  if ((s = check_codes(codes, axis == 1 ? cols : rows, ldc)) != FP4_OK) return s;
+  if ((s = check_scales(scales, sf_layout)) != FP4_OK) return s;
+  if (axis == 1 && rows * fp8_groups(cols) >= (int64_t)1 << 31) return FP4_ERR_SHAPE;      // 32-bit block index
+  if (axis == 0 && fp8_groups(rows) > kMaxTileRows) return FP4_ERR_SHAPE;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != FP4_OK) return s;
+  Fp8QuantizeParams p = {};
+  p.x = x;
+  p.rows = rows;
+  p.cols = cols;
+  p.ld = ld;
+  p.fmt = fmt;
+  p.sf_mma = sf_layout == FP4_SF_MMA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (axis == 1) {
+    p.codes = codes;
+    p.ldc = ldc;
+    p.scales = scales;
+    return from_cuda(launch_fp8_quantize_rows(p, sms, st));
+  }
+  p.codes_t = codes;
+  p.ldc_t = ldc;
+  p.scales_t = scales;
+  return from_cuda(launch_fp8_quantize_cols(p, st));
+}
+
+fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_t ld, int fmt, uint8_t* codes,
+                               int64_t ldc, uint8_t* scales, uint8_t* codes_t, int64_t ldc_t, uint8_t* scales_t,
+                               int sf_layout, void* stream) {
+  fp4_status s = check_input(x, rows, cols, ld);
+  if (s != FP4_OK) return s;
+  if (!fp8_format(fmt) || (codes_t == nullptr) != (scales_t == nullptr)) return FP4_ERR_ARG;
+  if ((s = check_codes(codes, cols, ldc)) != FP4_OK) return s;
+  if ((s = check_scales(scales, sf_layout)) != FP4_OK) return s;
+  if (codes_t != nullptr) {
+    if ((s = check_codes(codes_t, rows, ldc_t)) != FP4_OK) return s;
+    if ((s = check_scales(scales_t, sf_layout)) != FP4_OK) return s;
+  }
+  if (fp8_groups(rows) > kMaxTileRows) return FP4_ERR_SHAPE;
+  Fp8QuantizeParams p = {};
+  p.x = x;
+  p.rows = rows;
+  p.cols = cols;
+  p.ld = ld;
+  p.fmt = fmt;
+  p.codes = codes;
+  p.ldc = ldc;
+  p.scales = scales;
+  p.codes_t = codes_t;
+  p.ldc_t = ldc_t;
+  p.scales_t = scales_t;
+  p.sf_mma = sf_layout == FP4_SF_MMA;
+  return from_cuda(launch_fp8_quantize_tiles(p, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,
+                              int fmt, int sf_layout, void* out, int out_dtype, void* stream) {
+  if (rows <= 0 || cols <= 0 || out == nullptr || scales == nullptr) return FP4_ERR_ARG;
+  if (!fp8_format(fmt) || !sf_layout_ok(sf_layout)) return FP4_ERR_ARG;
+  if (out_dtype != FP4_OUT_F32 && out_dtype != FP4_OUT_BF16) return FP4_ERR_ARG;
+  fp4_status s = check_codes(codes, cols, ldc);
+  if (s != FP4_OK) return s;
+  if (rows >= (int64_t)1 << 31 || cols >= (int64_t)1 << 31) return FP4_ERR_SHAPE;
+  if (!aligned16(out)) return FP4_ERR_ALIGN;
+  return from_cuda(launch_fp8_dequantize(codes, ldc, scales, rows, cols, fmt, sf_layout == FP4_SF_MMA, out,
+                                         out_dtype == FP4_OUT_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+fp4_status fp4_fp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_sf, const uint8_t* b, int64_t ldb,
+                        const uint8_t* b_sf, int64_t M, int64_t N, int64_t K, int a_fmt, int b_fmt, void* y,
+                        int64_t ldy, int y_dtype, void* stream) {
+  if (M <= 0 || N <= 0 || K <= 0 || y == nullptr || a_sf == nullptr || b_sf == nullptr || ldy < N) return FP4_ERR_ARG;
+  if (!fp8_format(a_fmt) || !fp8_format(b_fmt)) return FP4_ERR_ARG;
+  if (y_dtype != FP4_OUT_F32 && y_dtype != FP4_OUT_BF16) return FP4_ERR_ARG;
+  fp4_status s = check_codes(a, K, lda);
+  if (s != FP4_OK) return s;
+  if ((s = check_codes(b, K, ldb)) != FP4_OK) return s;
+  // 32-bit indices of rows, blocks and tiles; row strides of a tensor map are below 2^40
+  constexpr int64_t kMost = ((int64_t)1 << 31) - 4096;
+  if (M > kMost || N > kMost || K > kMost || lda >= (int64_t)1 << 40 || ldb >= (int64_t)1 << 40) return FP4_ERR_SHAPE;
+  if (((M + 127) / 128) * ((N + 127) / 128) >= kMost / 8) return FP4_ERR_SHAPE;
+  if (!aligned16(a_sf) || !aligned16(b_sf)) return FP4_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(y) & (y_dtype == FP4_OUT_F32 ? 3u : 1u)) != 0) return FP4_ERR_ALIGN;
+  DeviceState* d = nullptr;
+  if ((s = device_state(&d)) != FP4_OK) return s;
+  Fp8GemmParams p;
+  p.a = a;
+  p.lda = lda;
+  p.a_sf = a_sf;
+  p.b = b;
+  p.ldb = ldb;
+  p.b_sf = b_sf;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.a_fmt = a_fmt;
+  p.b_fmt = b_fmt;
+  p.y = y;
+  p.ldy = ldy;
+  p.y_bf16 = y_dtype == FP4_OUT_BF16;
+  p.error = d->scratch.error;
+  const cudaError_t e = launch_fp8_gemm(p, d->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaErrorNotSupported ? FP4_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+fp4_status fp4_rmsnorm_fp8_quantize(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                    int weight_dtype, int64_t rows, int64_t cols, float eps, int fmt, uint8_t* codes,
+                                    int64_t ldc, uint8_t* scales, int sf_layout, void* residual_out, float* rstd,
+                                    void* norm_out, void* stream) {
+  fp4_status s = check_norm_shape(rows, cols, weight, weight_dtype);
+  if (s != FP4_OK) return s;
+  if (!fp8_format(fmt) || !(eps >= 0.0f && eps <= 3.402823466e+38f)) return FP4_ERR_ARG;
+  if ((residual == nullptr) != (residual_out == nullptr)) return FP4_ERR_ARG;
+  if ((s = check_rows16(x, cols, ldx)) != FP4_OK) return s;
+  if (residual != nullptr && (s = check_rows16(residual, cols, ldr)) != FP4_OK) return s;
+  if ((s = check_codes(codes, cols, ldc)) != FP4_OK) return s;
+  if ((s = check_scales(scales, sf_layout)) != FP4_OK) return s;
+  if (!aligned16(residual_out) || !aligned16(norm_out) || (reinterpret_cast<uintptr_t>(rstd) & 3u) != 0)
+    return FP4_ERR_ALIGN;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != FP4_OK) return s;
+  RmsNormParams p;
+  p.x = x;
+  p.ldx = ldx;
+  p.residual = residual;
+  p.ldr = ldr;
+  p.weight = weight;
+  p.weight_f32 = weight_dtype == FP4_OUT_F32;
+  p.rows = rows;
+  p.cols = cols;
+  p.eps = eps;
+  p.fmt = fmt;
+  p.codes = codes;
+  p.ldc = ldc;
+  p.scales = scales;
+  p.sf_mma = sf_layout == FP4_SF_MMA;
+  p.residual_out = residual_out;
+  p.rstd = rstd;
+  p.norm_out = norm_out;
+  return from_cuda(launch_rmsnorm_fp8(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp4_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+  int sms = 0;
+  if (rows <= 0 || cols <= 0 || cols % 8 != 0 || cols > kMaxNormCols || device_sms(&sms) != FP4_OK) return 0;
+  return sizeof(float) * (size_t)cols * (size_t)rmsnorm_backward_parts(rows, cols, sms);
+}
+
+fp4_status fp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                                int weight_dtype, const float* rstd, const void* dresidual, int64_t lddr, int64_t rows,
+                                int64_t cols, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  fp4_status s = check_norm_shape(rows, cols, weight, weight_dtype);
+  if (s != FP4_OK) return s;
+  if (rstd == nullptr || dx == nullptr || dweight == nullptr || workspace == nullptr) return FP4_ERR_ARG;
+  if ((s = check_rows16(dy, cols, lddy)) != FP4_OK) return s;
+  if ((s = check_rows16(h, cols, ldh)) != FP4_OK) return s;
+  if (dresidual != nullptr && (s = check_rows16(dresidual, cols, lddr)) != FP4_OK) return s;
+  if (!aligned16(dx) || !aligned16(dweight) || !aligned16(workspace)) return FP4_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(rstd) & 3u) != 0) return FP4_ERR_ALIGN;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != FP4_OK) return s;
+  if (workspace_bytes < sizeof(float) * (size_t)cols * (size_t)rmsnorm_backward_parts(rows, cols, sms))
+    return FP4_ERR_ARG;
+  RmsNormBackwardParams p;
+  p.dy = dy;
+  p.lddy = lddy;
+  p.h = h;
+  p.ldh = ldh;
+  p.weight = weight;
+  p.weight_f32 = weight_dtype == FP4_OUT_F32;
+  p.rstd = rstd;
+  p.dresidual = dresidual;
+  p.lddr = lddr;
+  p.rows = rows;
+  p.cols = cols;
+  p.dx = dx;
+  p.dweight = dweight;
+  p.partials = static_cast<float*>(workspace);
+  return from_cuda(launch_rmsnorm_backward(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fp4_fp8_scales_bytes(int64_t rows, int64_t cols, int axis, int sf_layout) {
+  if (rows <= 0 || cols <= 0 || (axis != 0 && axis != 1) || !sf_layout_ok(sf_layout)) return 0;
+  const int64_t orows = axis == 1 ? rows : cols, groups = fp8_groups(axis == 1 ? cols : rows);
+  if (sf_layout == FP4_SF_ROWMAJOR) return (size_t)(orows * groups);
+  return (size_t)(round_up(orows, 128) * round_up(groups, 4));
 }
 
 fp4_status fp4_amax(const void* x, int64_t rows, int64_t cols, int64_t ld, float* amax_out, void* stream) {

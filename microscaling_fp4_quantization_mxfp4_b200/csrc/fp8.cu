@@ -1,0 +1,353 @@
+// Block-scaled FP8 quantization (E4M3 / E5M2 codes, one E8M0 scale per 128 elements) and its inverse.
+// The formats and the scale rule are in fp8_device.cuh.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "fp4_device.cuh"
+#include "fp4_internal.h"
+#include "fp8_device.cuh"
+#include "fp8_internal.h"
+
+namespace fp4lib {
+namespace {
+
+using namespace fp8dev;
+
+// ------------------------------------------------------- blocks along rows --
+// Half a warp per block: 16 lanes x 8 elements (one 16-byte load each), the block's maximum by four
+// shuffles, 8-byte code stores (128 contiguous bytes a block).  Bound by HBM: 2 bytes in, 1 out per
+// element.  Each warp takes kUnroll pairs of adjacent blocks with all loads in flight at once.
+constexpr int kRowThreads = 256;
+constexpr int kUnroll = 4;
+
+struct RowArgs {
+  const uint16_t* x;
+  long long rows, ld, ldc;
+  uint8_t* codes;
+  uint8_t* scales;
+  uint32_t groups, chunks;      // 128-element blocks and 8-element chunks in a row
+  uint32_t items;               // rows * groups
+  uint32_t main_ctas;           // CTAs beyond these zero the scale rows that pad the tensor-core layout
+  int sf_mma;
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kRowThreads) fp8_quantize_rows_kernel(RowArgs p) {
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x >= p.main_ctas) {
+    zero_pad_rows(p.scales, p.rows, p.groups);
+    return;
+  }
+  const uint32_t lane = threadIdx.x & 31u, half = lane >> 4, c16 = lane & 15u;
+  const uint32_t warp = (blockIdx.x * kRowThreads + threadIdx.x) >> 5;
+  const uint32_t first = warp * (2 * kUnroll);
+  uint4 v[kUnroll];
+  uint32_t row[kUnroll], g[kUnroll];
+  bool on[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t it = first + 2 * u + half;
+    row[u] = it / p.groups;
+    g[u] = it - row[u] * p.groups;
+    on[u] = it < p.items && g[u] * 16 + c16 < p.chunks;
+    v[u] = make_uint4(0, 0, 0, 0);
+    if (on[u]) v[u] = *reinterpret_cast<const uint4*>(p.x + (long long)row[u] * p.ld + (g[u] * 16 + c16) * 8);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t byte = scale_byte<FMT>(max_half_warp(pair_bits(max_abs8(v[u]))));
+    const float inv = inv_scale(byte);
+    float e[8];
+    fp4dev::unpack8(v[u], e);
+    if (on[u])
+      *reinterpret_cast<uint2*>(p.codes + (long long)row[u] * p.ldc + (g[u] * 16 + c16) * 8) = codes8<FMT>(e, inv);
+    if (first + 2 * u + half < p.items) {
+      if (c16 == 0) {
+        p.scales[sf_offset(p.sf_mma, row[u], g[u], p.groups)] = (uint8_t)byte;
+      } else if (p.sf_mma && g[u] + 1 == p.groups && c16 <= ((4u - (p.groups & 3u)) & 3u)) {
+        p.scales[sf_offset(1, row[u], g[u] + c16, p.groups)] = 0;       // groups that pad the layout to 4
+      }
+    }
+  }
+}
+
+// ------------------------------------------- blocks along columns, and tiles --
+// A CTA takes 128 x 128 elements: eight 16-byte loads a thread, kept in registers and copied to shared
+// memory.  TILE = false: every column of the tile is one block of the transpose.  TILE = true: one
+// scale for the tile; the row codes are made from the registers, the transpose's from shared memory.
+// In the column phase a lane reads two adjacent columns (32 lanes: 64 columns, no bank conflicts) of
+// 32 rows, so that its codes of a column are 32 contiguous bytes of the transpose.
+constexpr int kTileThreads = 256;
+constexpr int kTileLoads = 8;           // 16-byte chunks a thread
+
+struct TileArgs {
+  const uint16_t* x;
+  long long rows, cols, ld, ldc, ldc_t;
+  uint8_t* codes;
+  uint8_t* scales;
+  uint8_t* codes_t;
+  uint8_t* scales_t;
+  long long groups, groups_t;
+  int sf_mma;
+};
+
+// 32 codes of one column into the transpose's row `dst` (32 elements, `n` of them inside).
+__device__ __forceinline__ void store_codes32(uint8_t* dst, const uint32_t (&w)[8], int n) {
+  if (n >= 32) {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) dst[i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+  }
+}
+
+template <int FMT, bool TILE>
+__global__ void __launch_bounds__(kTileThreads) fp8_quantize_tile_kernel(TileArgs p) {
+  pdl_trigger();
+  __shared__ uint32_t tile[128 * 64];             // bf16 pairs, row-major
+  __shared__ uint32_t red[4 * 64];                // column maxima of the four 32-row groups / warps' maxima
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const long long rt = blockIdx.y, ct = blockIdx.x;              // row and column tile
+  const long long r0 = rt * 128, c0 = ct * 128;
+  pdl_wait();
+  if (r0 >= p.rows || c0 >= p.cols) {
+    // a tile of the layout's padding: its scales are zero
+    if (t < 128) {
+      if (TILE && r0 < p.rows) p.scales[sf_offset(1, r0 + t, ct, p.groups)] = 0;
+      if (c0 < p.cols && p.scales_t != nullptr) p.scales_t[sf_offset(1, c0 + t, rt, p.groups_t)] = 0;
+    }
+    return;
+  }
+  uint4 v[kTileLoads];
+#pragma unroll
+  for (int i = 0; i < kTileLoads; ++i) {
+    const int r = (t >> 4) + 16 * i, c = (t & 15) * 8;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r0 + r < p.rows && c0 + c < p.cols)
+      v[i] = *reinterpret_cast<const uint4*>(p.x + (r0 + r) * p.ld + c0 + c);
+  }
+  const bool want_t = !TILE || p.codes_t != nullptr;
+  if (want_t) {
+#pragma unroll
+    for (int i = 0; i < kTileLoads; ++i)
+      *reinterpret_cast<uint4*>(&tile[((t >> 4) + 16 * i) * 64 + (t & 15) * 4]) = v[i];
+  }
+  uint32_t byte = 0;
+  if (TILE) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kTileLoads; ++i) m = __vmaxu2(m, max_abs8(v[i]));
+    m = __reduce_max_sync(0xFFFFFFFFu, pair_bits(m));
+    if (lane == 0) red[warp] = m;
+  }
+  __syncthreads();
+  if (TILE) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < kTileThreads / 32; ++w) m = max(m, red[w]);
+    byte = scale_byte<FMT>(m);
+    const float inv = inv_scale(byte);
+#pragma unroll
+    for (int i = 0; i < kTileLoads; ++i) {
+      const int r = (t >> 4) + 16 * i, c = (t & 15) * 8;
+      if (r0 + r < p.rows && c0 + c < p.cols) {
+        float e[8];
+        fp4dev::unpack8(v[i], e);
+        *reinterpret_cast<uint2*>(p.codes + (r0 + r) * p.ldc + c0 + c) = codes8<FMT>(e, inv);
+      }
+    }
+    if (t < 128) {
+      if (r0 + t < p.rows) p.scales[sf_offset(p.sf_mma, r0 + t, ct, p.groups)] = (uint8_t)byte;
+      else if (p.sf_mma) p.scales[sf_offset(1, r0 + t, ct, p.groups)] = 0;
+    }
+    if (!want_t) return;
+  }
+  // columns: lane -> pair of columns in half `warp & 1`, rows 32 * (warp >> 1) .. + 31
+  const int pr = (warp & 1) * 32 + lane, rg = warp >> 1;
+  uint32_t w[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) w[i] = tile[(rg * 32 + i) * 64 + pr];
+  uint32_t blo = byte, bhi = byte;
+  if (!TILE) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max_abs2(m, w[i]);
+    red[rg * 64 + pr] = m;
+    __syncthreads();
+    m = __vmaxu2(__vmaxu2(red[pr], red[64 + pr]), __vmaxu2(red[128 + pr], red[192 + pr]));
+    blo = scale_byte<FMT>(m << 16);
+    bhi = scale_byte<FMT>(m & 0xFFFF0000u);
+  }
+  const float ilo = inv_scale(blo), ihi = inv_scale(bhi);
+  const long long c = c0 + 2 * pr;                        // even, and cols is a multiple of 8: both inside or both out
+  if (c < p.cols) {
+    uint32_t lo[8], hi[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      lo[k] = cvt4<FMT>(__fmul_rn(fp4dev::bf16_lo(w[4 * k]), ilo), __fmul_rn(fp4dev::bf16_lo(w[4 * k + 1]), ilo),
+                        __fmul_rn(fp4dev::bf16_lo(w[4 * k + 2]), ilo), __fmul_rn(fp4dev::bf16_lo(w[4 * k + 3]), ilo));
+      hi[k] = cvt4<FMT>(__fmul_rn(fp4dev::bf16_hi(w[4 * k]), ihi), __fmul_rn(fp4dev::bf16_hi(w[4 * k + 1]), ihi),
+                        __fmul_rn(fp4dev::bf16_hi(w[4 * k + 2]), ihi), __fmul_rn(fp4dev::bf16_hi(w[4 * k + 3]), ihi));
+    }
+    const long long left = p.rows - (r0 + rg * 32);
+    if (left > 0) {
+      uint8_t* dst = p.codes_t + c * p.ldc_t + r0 + rg * 32;
+      const int n = left < 32 ? (int)left : 32;
+      store_codes32(dst, lo, n);
+      store_codes32(dst + p.ldc_t, hi, n);
+    }
+    if (rg == 0) {
+      p.scales_t[sf_offset(p.sf_mma, c, rt, p.groups_t)] = (uint8_t)blo;
+      p.scales_t[sf_offset(p.sf_mma, c + 1, rt, p.groups_t)] = (uint8_t)bhi;
+    }
+  } else if (p.sf_mma && rg == 0) {
+    p.scales_t[sf_offset(1, c, rt, p.groups_t)] = 0;
+    p.scales_t[sf_offset(1, c + 1, rt, p.groups_t)] = 0;
+  }
+}
+
+// ------------------------------------------------------------- dequantize --
+// One thread per 8 codes of a row: value = code * 2^(byte - 127) in fp32 (exact wherever the product
+// is a normal fp32 number), rounded to bf16 on request.
+struct DeqArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* out;
+  long long rows, cols, ldc;
+  uint32_t chunks, groups;
+  uint64_t items;
+  int sf_mma, fmt, out_bf16, vec;
+};
+
+__device__ __forceinline__ float code_value(uint32_t c, int fmt) {
+  uint32_t h2;
+  if (fmt == 0) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)c));
+  else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)c));
+  const uint16_t h = (uint16_t)h2;
+  return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+__global__ void __launch_bounds__(256) fp8_dequantize_kernel(DeqArgs p) {
+  pdl_trigger();
+  pdl_wait();
+  for (uint64_t it = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; it < p.items;
+       it += (uint64_t)gridDim.x * blockDim.x) {
+    const uint64_t row = it / p.chunks;
+    const uint32_t c = (uint32_t)(it - row * p.chunks) * 8;
+    const uint32_t byte = p.scales[sf_offset(p.sf_mma, (long long)row, c >> 7, p.groups)];
+    const float s = byte == kNanByte ? __uint_as_float(0x7FFFFFFFu) : fp4dev::mx_scale_value(byte);
+    const uint2 q = *reinterpret_cast<const uint2*>(p.codes + row * p.ldc + c);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = i < 4 ? q.x : q.y;
+      v[i] = __fmul_rn(code_value((w >> (8 * (i & 3))) & 0xFFu, p.fmt), s);
+    }
+    const long long o = (long long)row * p.cols + c;
+    if (p.out_bf16) {
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out) + o;
+      if (p.vec) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * i])) |
+                 ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[2 * i + 1])) << 16);
+        *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        for (int i = 0; i < 8; ++i)
+          if (c + i < p.cols) y[i] = __float2bfloat16_rn(v[i]);
+      }
+    } else {
+      float* y = static_cast<float*>(p.out) + o;
+      if (p.vec) {
+        reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        for (int i = 0; i < 8; ++i)
+          if (c + i < p.cols) y[i] = v[i];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize_rows(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
+  (void)num_sms;
+  RowArgs p;
+  p.x = static_cast<const uint16_t*>(q.x);
+  p.rows = q.rows;
+  p.ld = q.ld;
+  p.ldc = q.ldc;
+  p.codes = q.codes;
+  p.scales = q.scales;
+  p.groups = (uint32_t)fp8_groups(q.cols);
+  p.chunks = (uint32_t)(q.cols / 8);
+  p.items = (uint32_t)(q.rows * p.groups);
+  p.sf_mma = q.sf_mma;
+  constexpr uint32_t per_cta = kRowThreads / 32 * 2 * kUnroll;
+  p.main_ctas = (p.items + per_cta - 1) / per_cta;
+  const uint32_t grid = p.main_ctas + (q.sf_mma && q.rows % 128 != 0 ? 1u : 0u);
+  return q.fmt == FP8_E4M3_CODES
+             ? launch_kernel(fp8_quantize_rows_kernel<0>, dim3(grid), dim3(kRowThreads), 0, st, false, 1u, p)
+             : launch_kernel(fp8_quantize_rows_kernel<1>, dim3(grid), dim3(kRowThreads), 0, st, false, 1u, p);
+}
+
+template <bool TILE>
+static cudaError_t launch_tiles(const Fp8QuantizeParams& q, cudaStream_t st) {
+  TileArgs p;
+  p.x = static_cast<const uint16_t*>(q.x);
+  p.rows = q.rows;
+  p.cols = q.cols;
+  p.ld = q.ld;
+  p.ldc = q.ldc;
+  p.ldc_t = q.ldc_t;
+  p.codes = q.codes;
+  p.scales = q.scales;
+  p.codes_t = q.codes_t;
+  p.scales_t = q.scales_t;
+  p.groups = fp8_groups(q.cols);
+  p.groups_t = fp8_groups(q.rows);
+  p.sf_mma = q.sf_mma;
+  int64_t gx = p.groups, gy = p.groups_t;
+  if (q.sf_mma) {                     // the groups that pad the layout to 4 are tiles of their own
+    if (TILE) gx = (gx + 3) / 4 * 4;
+    if (q.scales_t != nullptr) gy = (gy + 3) / 4 * 4;
+  }
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  return q.fmt == FP8_E4M3_CODES
+             ? launch_kernel(fp8_quantize_tile_kernel<0, TILE>, grid, dim3(kTileThreads), 0, st, false, 1u, p)
+             : launch_kernel(fp8_quantize_tile_kernel<1, TILE>, grid, dim3(kTileThreads), 0, st, false, 1u, p);
+}
+
+cudaError_t launch_fp8_quantize_cols(const Fp8QuantizeParams& q, cudaStream_t st) { return launch_tiles<false>(q, st); }
+cudaError_t launch_fp8_quantize_tiles(const Fp8QuantizeParams& q, cudaStream_t st) { return launch_tiles<true>(q, st); }
+
+cudaError_t launch_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,
+                                  int fmt, int sf_mma, void* out, int out_bf16, cudaStream_t st) {
+  DeqArgs p;
+  p.codes = codes;
+  p.scales = scales;
+  p.out = out;
+  p.rows = rows;
+  p.cols = cols;
+  p.ldc = ldc;
+  p.chunks = (uint32_t)((cols + 7) / 8);
+  p.groups = (uint32_t)fp8_groups(cols);
+  p.items = (uint64_t)rows * p.chunks;
+  p.sf_mma = sf_mma;
+  p.fmt = fmt;
+  p.out_bf16 = out_bf16;
+  p.vec = cols % 8 == 0;
+  const uint64_t ctas = (p.items + 255) / 256;
+  const unsigned grid = (unsigned)std::min<uint64_t>(ctas, 1u << 20);
+  return launch_kernel(fp8_dequantize_kernel, dim3(grid), dim3(256), 0, st, false, 1u, p);
+}
+
+}  // namespace fp4lib

@@ -1,0 +1,483 @@
+// Block-scaled FP8 x FP8 product with fp32 accumulation on the sm_100a tensor cores (tcgen05), fed by TMA.
+//
+//   Y[M,N] = sum over 128-element blocks kb of 2^(ea[m,kb] + eb[n,kb]) * sum_{k in kb} a[m,k] * b[n,k]
+//
+// with A and B in E4M3 or E5M2 (each its own), both along K, and the E8M0 bytes of their 1 x 128 blocks
+// (or 128 x 128 tiles, whose byte every row repeats) in the tensor-core scale layout.
+//
+// kind::mxf8f6f4 scales 32 elements of K by one byte of a row's 32-bit scale word, the byte chosen by
+// the instruction.  The four K = 32 instructions of a 128-element block all name the same byte, so the
+// layout holds one byte a block and one 512-byte atom (128 rows x 4 bytes) serves 512 elements of K: a
+// quarter of the scale bytes, and of the copies into tensor memory, that 32-element blocks need.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "fp4_device.cuh"
+#include "fp4_internal.h"
+#include "fp8_internal.h"
+#include "gemm_device.cuh"
+
+namespace fp4lib {
+using namespace fp4tc;
+namespace {
+
+constexpr int kBK = 128;                  // elements (= bytes) of K per stage: one scale block
+constexpr uint32_t kCols = 512;           // tensor memory columns
+constexpr uint32_t kScaleBufs = 4;        // scale buffers (512 elements of K each), shared memory and tensor memory
+constexpr int kRing = 216 * 1024;
+
+struct Fp8KernelArgs {
+  const uint8_t* a_sf;
+  const uint8_t* b_sf;
+  void* y;
+  long long ldy;
+  int M, N, K;
+  int num_m, num_n;
+  int g4;                                 // 512-element scale atoms along K
+  uint32_t a_type, b_type;                // 0 E4M3, 1 E5M2
+  int vec_store;                          // output rows 16-byte aligned
+  unsigned* error;
+};
+
+// A: the 128 (or, over an SM pair, 256) rows of the accumulator; B: its n columns.  `id`: the byte of
+// the scale words that this block's instructions use.
+__device__ __forceinline__ uint32_t fp8_idesc(uint32_t m, uint32_t n, uint32_t a_type, uint32_t b_type, uint32_t id) {
+  return (id << 4) | (a_type << 7) | (b_type << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 7) << 27) | (id << 29);
+}
+__device__ __forceinline__ void fp8_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+// ------------------------------------------------- tiles of Y^T over clusters --
+// Y^T = B . A^T in tiles of 128 rows of B by BNT rows of A (16 to 256), so that a product with few
+// activation rows fills the MMA's 128 rows with weights and reads each of them once.  A tile's blocks
+// of K are divided over a cluster of `split` CTAs; each CTA accumulates its share in tensor memory, the
+// epilogue warps park it in the idle stage ring (one row per row of A), and after a cluster barrier
+// every CTA adds one slice over the cluster through distributed shared memory, in rank order, and
+// stores rows of Y.  Both cluster barriers are reached on every path, errors included.
+//
+// warp 0 TMA producer, warp 1 MMA issuer (one thread each), warps 2-5 epilogue, warp 6 scale copies.
+namespace tiles {
+
+constexpr int kMaxSplit = 8;
+
+template <int BNT>
+struct Cfg {
+  static constexpr int kThreads = 224;
+  static constexpr int kWBytes = 128 * kBK;
+  static constexpr int kXBytes = BNT * kBK;
+  static constexpr int kXAtoms = (BNT + 127) / 128;
+  static constexpr int kScaleBytes = (1 + kXAtoms) * 512;
+  static constexpr int kStageBytes = kWBytes + kXBytes;
+  static constexpr int kStages = std::min((kRing - (int)kScaleBufs * kScaleBytes) / kStageBytes, 12);
+  static constexpr int kPStride = 128 + 4;                       // floats of a parked row
+  static constexpr int kRingBytes =
+      kStages * kStageBytes > BNT * kPStride * 4 ? kStages * kStageBytes : BNT * kPStride * 4;
+  static constexpr int kSmem = 1024 + kRingBytes + (int)kScaleBufs * kScaleBytes + 512;
+  static constexpr uint32_t kScaleCol = 256;                     // scale buffers after the accumulator
+  static constexpr uint32_t kScaleCols = 16;                     // B's 4 columns, then A's 4 or 8
+};
+
+template <int BNT, bool BF16>
+__global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
+    fp8_gemm_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
+                         Fp8KernelArgs p, int split) {
+  using C = Cfg<BNT>;
+  constexpr int S = C::kStages;
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sW = smem;
+  uint8_t* sX = sW + S * C::kWBytes;
+  float* part = reinterpret_cast<float*>(smem);                  // reuses the ring after the last MMA
+  uint8_t* sScale = smem + C::kRingBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kScaleBufs * C::kScaleBytes);
+  uint64_t* full = bars;
+  uint64_t* empty = full + S;
+  uint64_t* sload = empty + S;                                   // scale buffer in shared memory
+  uint64_t* sfull = sload + kScaleBufs;                          // ... in tensor memory
+  uint64_t* sempty = sfull + kScaleBufs;                         // ... read by its last MMA
+  uint64_t* tfull = sempty + kScaleBufs;
+  uint64_t* drain = tfull + 1;
+  uint64_t* sdrain = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = split > 1 ? cluster_rank() : 0u;
+  const int tile = (int)(blockIdx.x / (uint32_t)split);
+  const int nt = tile % p.num_n, mt = tile / p.num_n;
+  const int nkb = (p.K + kBK - 1) / kBK;
+  const int kb0 = (int)((int64_t)nkb * rank / split), kb1 = (int)((int64_t)nkb * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (uint32_t b = 0; b < kScaleBufs; ++b) {
+      mbar_init(smem_u32(&sload[b]), 1);
+      mbar_init(smem_u32(&sfull[b]), 1);
+      mbar_init(smem_u32(&sempty[b]), 1);
+    }
+    mbar_init(smem_u32(tfull), 1);
+    mbar_init(smem_u32(drain), 1);
+    mbar_init(smem_u32(sdrain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();                               // the previous kernel's outputs (our operands) are complete
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer --
+    if (lane == 0) {
+      const int x_atoms = min(C::kXAtoms, (p.M + 127) / 128 - mt * C::kXAtoms);
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_parity = 0, ns = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (kb == kb0 || (kb & 3) == 0) {                        // a new 512-element scale buffer
+          const uint32_t b = ns % kScaleBufs, use = ns / kScaleBufs;
+          ++ns;
+          if (!wait_spin(smem_u32(&sempty[b]), (use & 1u) ^ 1u, abort_flag)) {
+            raise_abort(abort_flag, p.error);
+            ok = false;
+            break;
+          }
+          const uint32_t lb = smem_u32(&sload[b]);
+          uint8_t* dst = sScale + b * C::kScaleBytes;
+          mbar_expect_tx(lb, (uint32_t)(512 * (1 + x_atoms)));
+          bulk_load(smem_u32(dst), p.b_sf + ((size_t)nt * p.g4 + (kb >> 2)) * 512, 512u, lb);
+          for (int i = 0; i < x_atoms; ++i)
+            bulk_load(smem_u32(dst + 512 * (1 + i)),
+                      p.a_sf + ((size_t)(mt * C::kXAtoms + i) * p.g4 + (kb >> 2)) * 512, 512u, lb);
+        }
+        if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+          raise_abort(abort_flag, p.error);
+          ok = false;
+          break;
+        }
+        const uint32_t fb = smem_u32(&full[stage]);
+        mbar_expect_tx(fb, (uint32_t)C::kStageBytes);
+        tma_load_2d(smem_u32(sW + stage * C::kWBytes), &tmap_w, kb * kBK, nt * 128, fb);
+        tma_load_2d(smem_u32(sX + stage * C::kXBytes), &tmap_x, kb * kBK, mt * BNT, fb);
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        // let every copy already issued land before the CTA can exit
+        volatile int never = 0;
+        for (int s = 0; s < S; ++s)
+          if (issued & (1u << s)) wait_bounded(smem_u32(&full[s]), (issued_parity >> s) & 1u, &never);
+        for (uint32_t i = ns > kScaleBufs ? ns - kScaleBufs : 0; i < ns; ++i)
+          wait_bounded(smem_u32(&sload[i % kScaleBufs]), (i / kScaleBufs) & 1u, &never);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer --
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, ns = 0;
+      bool ok = true, any_mma = false;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (kb == kb0 || (kb & 3) == 0) {
+          if (!wait_spin(smem_u32(&sfull[ns % kScaleBufs]), (ns / kScaleBufs) & 1u, abort_flag)) {
+            raise_abort(abort_flag, p.error);
+            ok = false;
+            break;
+          }
+          ++ns;
+        }
+        if (!wait_spin(smem_u32(&full[stage]), phase, abort_flag)) {
+          raise_abort(abort_flag, p.error);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t b = (ns - 1) % kScaleBufs;
+        const uint32_t sw = tmem + C::kScaleCol + b * C::kScaleCols, sx = sw + 4u;
+        const uint64_t wdesc = desc_sw128(smem_u32(sW + stage * C::kWBytes));
+        const uint64_t xdesc = desc_sw128(smem_u32(sX + stage * C::kXBytes));
+        const uint32_t idesc = fp8_idesc(128, BNT, p.b_type, p.a_type, (uint32_t)(kb & 3));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          fp8_mma(tmem, wdesc + (uint64_t)(2 * j), xdesc + (uint64_t)(2 * j), idesc, sw, sx, (kb > kb0 || j > 0) ? 1u : 0u);
+        any_mma = true;
+        tc_commit(smem_u32(&empty[stage]));
+        if ((kb & 3) == 3 || kb + 1 == kb1) tc_commit(smem_u32(&sempty[b]));
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok) {
+        tc_commit(smem_u32(tfull));
+      } else if (any_mma) {
+        // the MMAs already issued end before tensor memory is released
+        tc_commit(smem_u32(drain));
+        volatile int never = 0;
+        wait_bounded(smem_u32(drain), 0u, &never);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // -------------------------------------------------------- scale copies --
+    if (lane == 0) {
+      uint32_t ns = 0;
+      bool ok = true, any_cp = false;
+      for (int kb = kb0; kb < kb1; kb = (kb & ~3) + 4, ++ns) {
+        const uint32_t b = ns % kScaleBufs;
+        if (!wait_spin(smem_u32(&sload[b]), (ns / kScaleBufs) & 1u, abort_flag)) {
+          raise_abort(abort_flag, p.error);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sw = tmem + C::kScaleCol + b * C::kScaleCols;
+        uint8_t* src = sScale + b * C::kScaleBytes;
+#pragma unroll
+        for (int i = 0; i <= C::kXAtoms; ++i) tc_cp_sf(sw + 4u * i, desc_sf(smem_u32(src + 512 * i)));
+        tc_commit(smem_u32(&sfull[b]));
+        any_cp = true;
+      }
+      if (!ok && any_cp) {
+        tc_commit(smem_u32(sdrain));
+        volatile int never = 0;
+        wait_bounded(smem_u32(sdrain), 0u, &never);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------- this CTA's share, one row per row of A --
+    // warp w reads tensor-memory lanes 32 * (w % 4) .. + 31 (rows of B) and all BNT columns
+    const int q = warp & 3;
+    int ok = 1;
+    if (lane == 0) ok = wait_bounded(smem_u32(tfull), 0u, abort_flag) ? 1 : 0;
+    ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    if (!ok) {
+      if (lane == 0) raise_abort(abort_flag, p.error);
+    } else {
+      tc_fence_after();
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // ring bytes last touched by the async proxy
+      float* col = part + q * 32 + lane;
+      if (BNT == 16) {
+        uint32_t r[16];
+        tmem_ld16(tbase, r);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
+                     "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                     "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+#pragma unroll
+        for (int m = 0; m < 16; ++m) col[m * C::kPStride] = __uint_as_float(r[m]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < BNT / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tbase + (uint32_t)(32 * c), r);
+          asm volatile("tcgen05.wait::ld.sync.aligned;"
+                       : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                         "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                         "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                         "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                         "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+#pragma unroll
+          for (int i = 0; i < 32; ++i) col[(32 * c + i) * C::kPStride] = __uint_as_float(r[i]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync_all();        // every CTA's share is in its shared memory
+
+  // ------------------------------------------- add one slice over the cluster --
+  {
+    const int rows = min(BNT, p.M - mt * BNT), nvalid = min(128, p.N - nt * 128);
+    const int c4n = (nvalid + 3) / 4;                              // groups of four columns of Y
+    const int items = rows * c4n;
+    const int i0 = (int)((int64_t)items * rank / split), i1 = (int)((int64_t)items * (rank + 1) / split);
+    const uint32_t part_base = smem_u32(part);
+    for (int it = i0 + (int)threadIdx.x; it < i1; it += (int)blockDim.x) {
+      const int r = it / c4n, c4 = it - r * c4n;
+      float4 acc;
+      if (split == 1) {
+        acc = *reinterpret_cast<const float4*>(part + r * C::kPStride + 4 * c4);
+      } else {
+        const uint32_t addr = part_base + (uint32_t)((r * C::kPStride + 4 * c4) * 4);
+        float4 v[kMaxSplit];                                       // all remote loads in flight at once
+#pragma unroll
+        for (int s = 0; s < kMaxSplit; ++s)
+          if (s < split) v[s] = ld_cluster_f4(map_rank(addr, (uint32_t)s));
+        acc = v[0];
+#pragma unroll
+        for (int s = 1; s < kMaxSplit; ++s)
+          if (s < split) {
+            acc.x = __fadd_rn(acc.x, v[s].x);
+            acc.y = __fadd_rn(acc.y, v[s].y);
+            acc.z = __fadd_rn(acc.z, v[s].z);
+            acc.w = __fadd_rn(acc.w, v[s].w);
+          }
+      }
+      const float y4[4] = {acc.x, acc.y, acc.z, acc.w};
+      const int n0 = nt * 128 + 4 * c4;
+      const long long o = (long long)(mt * BNT + r) * p.ldy + n0;
+      if (BF16) {
+        __nv_bfloat16* yr = static_cast<__nv_bfloat16*>(p.y) + o;
+        if (p.vec_store && n0 + 4 <= p.N) {
+          *reinterpret_cast<uint2*>(yr) =
+              make_uint2((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[0])) |
+                             ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[1])) << 16),
+                         (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[2])) |
+                             ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[3])) << 16));
+        } else {
+          for (int i = 0; i < 4; ++i)
+            if (n0 + i < p.N) yr[i] = __float2bfloat16_rn(y4[i]);
+        }
+      } else {
+        float* yr = static_cast<float*>(p.y) + o;
+        if (p.vec_store && n0 + 4 <= p.N) {
+          *reinterpret_cast<float4*>(yr) = acc;
+        } else {
+          for (int i = 0; i < 4; ++i)
+            if (n0 + i < p.N) yr[i] = y4[i];
+        }
+      }
+    }
+  }
+  if (split > 1) cluster_sync_all();        // no CTA leaves while a peer may still read its share
+  tc_fence_after();
+  __syncthreads();
+  if (warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+  }
+}
+
+}  // namespace tiles
+
+// ------------------------------------------------------------------ host ---
+// [rows, k] bytes with row pitch ld: boxes of 128 bytes x box_rows, 128B swizzle.  The map ends at k, so
+// the elements of the last block that lie past it read as zero whatever the row's padding holds.
+bool code_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t k, int64_t ld, int box_rows) {
+  auto enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+Fp8KernelArgs kernel_args(const Fp8GemmParams& q) {
+  Fp8KernelArgs p;
+  p.a_sf = q.a_sf;
+  p.b_sf = q.b_sf;
+  p.y = q.y;
+  p.ldy = q.ldy;
+  p.M = (int)q.M;
+  p.N = (int)q.N;
+  p.K = (int)q.K;
+  p.num_m = p.num_n = 0;
+  p.g4 = (int)((fp8_groups(q.K) + 3) / 4);
+  p.a_type = (uint32_t)q.a_fmt;
+  p.b_type = (uint32_t)q.b_fmt;
+  const int64_t esz = q.y_bf16 ? 2 : 4;
+  p.vec_store = (q.ldy * esz) % 16 == 0 && (reinterpret_cast<uintptr_t>(q.y) & 15u) == 0;
+  p.error = q.error;
+  return p;
+}
+
+// Clusters of `split` CTAs of this kernel that the device holds at once (0 if unknown).
+template <int BNT, bool BF16>
+int max_clusters(int split) {
+  using C = tiles::Cfg<BNT>;
+  static std::mutex mu;
+  static int cache[tiles::kMaxSplit + 1] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[split] == 0) {
+    auto kernel = tiles::fp8_gemm_tile_kernel<BNT, BF16>;
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3((unsigned)C::kThreads);
+    cfg.dynamicSmemBytes = (size_t)C::kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = -1;
+    cache[split] = n;
+  }
+  return cache[split] > 0 ? cache[split] : 0;
+}
+
+template <int BNT, bool BF16>
+cudaError_t run_tiles(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
+  using C = tiles::Cfg<BNT>;
+  static_assert(C::kStages >= 2 && C::kSmem <= 227 * 1024, "shared memory");
+  auto kernel = tiles::fp8_gemm_tile_kernel<BNT, BF16>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (attr != cudaSuccess) return attr;
+  CUtensorMap tw, tx;
+  if (!code_map(&tw, q.b, q.N, q.K, q.ldb, 128)) return cudaErrorNotSupported;
+  if (!code_map(&tx, q.a, q.M, q.K, q.lda, BNT)) return cudaErrorNotSupported;
+  Fp8KernelArgs p = kernel_args(q);
+  p.num_m = (int)((q.M + BNT - 1) / BNT);
+  p.num_n = (int)((q.N + 127) / 128);
+  const int64_t n = (int64_t)p.num_m * p.num_n, nkb = fp8_groups(q.K);
+  // as many CTAs a tile as leave at most one CTA a SM, none without a block of K, and every cluster
+  // resident at once
+  int64_t split = std::max<int64_t>(1, std::min<int64_t>({num_sms / n, (int64_t)tiles::kMaxSplit, nkb}));
+  while (split > 1 && n > max_clusters<BNT, BF16>((int)split)) --split;
+  return launch_kernel(kernel, dim3((unsigned)(n * split)), dim3(C::kThreads), C::kSmem, st, false, (unsigned)split, tw,
+                       tx, p, (int)split);
+}
+
+template <bool BF16>
+cudaError_t dispatch(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
+  if (q.M <= 16) return run_tiles<16, BF16>(q, num_sms, st);
+  if (q.M <= 32) return run_tiles<32, BF16>(q, num_sms, st);
+  if (q.M <= 64) return run_tiles<64, BF16>(q, num_sms, st);
+  if (q.M <= 128) return run_tiles<128, BF16>(q, num_sms, st);
+  return run_tiles<256, BF16>(q, num_sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
+  return q.y_bf16 ? dispatch<true>(q, num_sms, st) : dispatch<false>(q, num_sms, st);
+}
+
+}  // namespace fp4lib

@@ -1,0 +1,234 @@
+"""8-bit quantizers and products on the GPU against the 64-bit oracle."""
+import numpy as np
+import pytest
+import torch
+
+import microscaling_fp4_quantization_mxfp4_b200 as fp
+from oracle import fp8, sf_from_mma
+
+pytestmark = pytest.mark.gpu
+
+
+def _input(rows, cols, seed, ld=None):
+    """bf16 [rows, cols] in rows of `ld` with changing magnitudes, a zero block, -0 and subnormal elements."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randint(-40, 40, (rows, 1), generator=g).float())
+    x[0, :128] = 0.0
+    x[rows // 2, : min(cols, 24)] = -0.0
+    x[rows - 1, cols // 2:] = 1e-39
+    buf = torch.full((rows, ld or cols), float("nan"), dtype=torch.bfloat16)
+    buf[:, :cols] = x.to(torch.bfloat16)
+    return buf.cuda()[:, :cols]
+
+
+def _f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _check(q, x64, fmt, tile, sf):
+    """Codes and scales bit for bit, the layout's padding included."""
+    codes, byte = fp8.quantize(x64, fmt, tile)
+    assert np.array_equal(q.codes.cpu().numpy(), codes)
+    s = q.scales.cpu().numpy()
+    assert np.array_equal(s, byte if sf == "rowmajor" else fp8.mma(byte))
+
+
+SHAPES = [(1, 8), (1, 128), (3, 120), (2, 136), (5, 384), (127, 1000), (128, 512), (129, 640), (300, 264), (1030, 520)]
+
+
+@pytest.mark.parametrize("sf", ["rowmajor", "mma"])
+@pytest.mark.parametrize("axis", [1, 0])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("rows, cols", SHAPES)
+def test_quantize(rows, cols, fmt, axis, sf):
+    x = _input(rows, cols, rows + cols, cols + (24 if rows % 2 else 0))
+    q = fp.fp4_fp8_quantize(x, fmt, axis, sf)
+    _check(q, _f64(x) if axis == 1 else _f64(x).T, fmt, False, sf)
+
+
+@pytest.mark.parametrize("sf", ["rowmajor", "mma"])
+@pytest.mark.parametrize("transposed", [True, False])
+@pytest.mark.parametrize("rows, cols", SHAPES)
+def test_quantize_2d(rows, cols, transposed, sf):
+    x = _input(rows, cols, rows * cols, cols + (8 if rows % 2 else 0))
+    for fmt in ("e4m3", "e5m2"):
+        q, t = fp.fp4_fp8_quantize_2d(x, fmt, sf, transposed)
+        _check(q, _f64(x), fmt, True, sf)
+        assert (t is not None) == transposed
+        if transposed:
+            _check(t, _f64(x).T, fmt, True, sf)
+
+
+@pytest.mark.parametrize("axis", [1, 0, 2])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_non_finite_blocks_are_nan(bad, axis):
+    x = _input(200, 264, 3)
+    x[70, 100], x[199, 263] = bad, bad
+    if axis == 2:
+        q = fp.fp4_fp8_quantize_2d(x)[0]
+        _check(q, _f64(x), "e4m3", True, "rowmajor")
+    else:
+        q = fp.fp4_fp8_quantize(x, axis=axis)
+        _check(q, _f64(x) if axis == 1 else _f64(x).T, "e4m3", False, "rowmajor")
+    d = fp.fp4_fp8_dequantize(q.codes, q.scales)
+    assert torch.isnan(d).sum() == (q.scales.repeat_interleave(128, 1)[:, : d.shape[1]] == 255).sum() > 0
+
+
+def test_bytes_past_the_rows_are_left_alone():
+    for axis, (rows, cols) in ((1, (37, 72)), (0, (37, 72))):
+        orows, length = (rows, cols) if axis == 1 else (cols, rows)
+        buf = torch.full((orows, 112), 0xA5, dtype=torch.uint8, device="cuda")
+        fp.fp4_fp8_quantize(_input(rows, cols, 1), axis=axis, codes=buf[:, :length])
+        assert torch.all(buf[:, length:] == 0xA5)
+    buf, buf_t = (torch.full((n, 112), 0xA5, dtype=torch.uint8, device="cuda") for n in (37, 72))
+    fp.fp4_fp8_quantize_2d(_input(37, 72, 1), codes=buf[:, :72], codes_t=buf_t[:, :37])
+    assert torch.all(buf[:, 72:] == 0xA5) and torch.all(buf_t[:, 37:] == 0xA5)
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sf", ["rowmajor", "mma"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("rows, cols", [(1, 1), (3, 127), (130, 136), (64, 1001)])
+def test_dequantize(rows, cols, fmt, sf, out_dtype):
+    g = np.random.default_rng(rows + cols)
+    codes = g.integers(0, 256, (rows, (cols + 15) // 16 * 16), dtype=np.uint8)
+    byte = g.integers(64, 190, (rows, -(-cols // 128)), dtype=np.uint8)
+    byte[0, 0] = 255
+    byte[rows - 1, -1] = 0
+    want = fp8.dequantize(codes[:, :cols], byte, fmt)
+    c = torch.from_numpy(codes).cuda()[:, :cols]
+    s = torch.from_numpy(byte if sf == "rowmajor" else fp8.mma(byte)).cuda()
+    got = fp.fp4_fp8_dequantize(c, s, fmt, sf, out_dtype)
+    want = torch.from_numpy(want).float() if out_dtype == "f32" else torch.from_numpy(want).float().to(torch.bfloat16)
+    assert torch.equal(torch.nan_to_num(got.cpu(), 7.0), torch.nan_to_num(want, 7.0))
+
+
+# ---------------------------------------------------------------- products --
+def _operand(rows, k, fmt, seed, tile=False):
+    g = np.random.default_rng(seed)
+    x = g.standard_normal((rows, k)) * np.exp2(g.integers(-6, 7, (rows, 1)))
+    codes, byte = fp8.quantize(x, fmt, tile)
+    c = torch.full((rows, (k + 15) // 16 * 16 + 16), 0x7F, dtype=torch.uint8)      # NaN past the row's end
+    c[:, :k] = torch.from_numpy(codes)
+    return c.cuda()[:, :k], torch.from_numpy(fp8.mma(byte)).cuda(), fp8.dequantize(codes, byte, fmt)
+
+
+def _bound(k, absum):
+    # products are exact in fp32 (8 significant bits at most, power-of-two scales); k of them are added in
+    # fp32 in some order, each addition off by at most one unit of the last place (2^-23; the tensor core need not
+    # round to nearest), so the sum is off by at most k * 2^-23 * sum |a b|, to first order
+    return (k + 8) * 2.0 ** -23 * absum
+
+
+def _check_gemm(M, N, K, a_fmt="e4m3", b_fmt="e4m3", seed=0, ldy=None):
+    a, sa, av = _operand(M, K, a_fmt, seed)
+    b, sb, bv = _operand(N, K, b_fmt, seed + 1, tile=True)
+    want, absum = fp8.gemm(av, bv)
+    for dtype in (torch.float32, torch.bfloat16):
+        buf = torch.full((M + 1, (ldy or N)), 77.0, dtype=dtype, device="cuda")
+        y = fp.fp4_fp8_gemm(a, sa, b, sb, a_fmt, b_fmt, out=buf[:M, :N])
+        fp.fp4_check_device_errors()
+        tol = _bound(K, absum) + (0 if dtype == torch.float32 else 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -8))
+        err = np.abs(_f64(y) - want)
+        assert np.all(err <= tol), (M, N, K, dtype, float((err / np.maximum(tol, 1e-300)).max()))
+        assert torch.all(buf[M:] == 77.0) and torch.all(buf[:, N:] == 77.0)
+
+
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64, 65, 100, 128, 129, 257])
+@pytest.mark.parametrize("N, K", [(1, 1), (128, 128), (136, 31), (300, 640), (257, 1000), (16, 4104)])
+def test_gemm(M, N, K):
+    _check_gemm(M, N, K, seed=M + N + K)
+
+
+@pytest.mark.parametrize("K", [16, 127, 129, 511, 512, 513, 1024, 1025, 2047, 5000])
+def test_gemm_lengths(K):
+    _check_gemm(40, 200, K, seed=K)
+
+
+@pytest.mark.parametrize("a_fmt, b_fmt", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("M, N, K", [(1, 130, 300), (70, 260, 999), (600, 520, 1032)])
+def test_gemm_types(M, N, K, a_fmt, b_fmt):
+    _check_gemm(M, N, K, a_fmt, b_fmt, seed=5)
+
+
+@pytest.mark.parametrize("M, N, K, ldy", [(3, 33, 256, 40), (3, 33, 256, 33), (200, 130, 256, 131), (700, 300, 640, 304)])
+def test_gemm_row_strides(M, N, K, ldy):
+    _check_gemm(M, N, K, seed=6, ldy=ldy)
+
+
+@pytest.mark.parametrize("M, N, K", [(2048, 2304, 768), (4096, 4096, 1024), (2500, 2700, 2200), (1000, 4096, 1500)])
+def test_gemm_large(M, N, K):
+    _check_gemm(M, N, K, seed=7)
+
+
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_gemm_nan_blocks_reach_their_rows_only(M):
+    a, sa, av = _operand(M, 300, "e4m3", 1)
+    b, sb, bv = _operand(260, 300, "e4m3", 2)
+    byte = sf_from_mma(sa.cpu().numpy(), M, 3)
+    byte[M - 1, 1] = 255
+    a[M - 1, 128:256] = 0x7F
+    y = fp.fp4_fp8_gemm(a, torch.from_numpy(fp8.mma(byte)).cuda(), b, sb)
+    nan = torch.isnan(y)
+    assert torch.all(nan[M - 1]) and not torch.any(nan[: M - 1])
+
+
+@pytest.mark.parametrize("M, N, K", [(1, 512, 512), (300, 512, 1024), (2048, 2048, 2048)])
+def test_gemm_repeats_bit_for_bit(M, N, K):
+    a, sa, _ = _operand(M, K, "e4m3", 1)
+    b, sb, _ = _operand(N, K, "e4m3", 2)
+    first = fp.fp4_fp8_gemm(a, sa, b, sb, out_dtype="f32")
+    for _ in range(3):
+        assert torch.equal(fp.fp4_fp8_gemm(a, sa, b, sb, out_dtype="f32"), first)
+
+
+def test_streams_and_graphs():
+    """Two streams at once, and the calls captured and replayed on new inputs, give the plain calls' bits."""
+    x = [torch.randn(300, 640, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    w = torch.randn(512, 640, device="cuda", dtype=torch.bfloat16)
+    wq = fp.fp4_fp8_quantize_2d(w, sf_layout="mma", transposed=False)[0]
+
+    def linear(t, stream=None):
+        q = fp.fp4_fp8_quantize(t, sf_layout="mma", stream=stream)
+        return fp.fp4_fp8_gemm(q.codes, q.scales, wq.codes, wq.scales, stream=stream)
+
+    want = [linear(t) for t in x]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [linear(t, s) for t, s in zip(x, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    static = x[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = linear(static)
+    for t, expect in ((x[1], want[1]), (x[0], want[0])):
+        static.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, expect)
+
+
+def test_binding_refusals():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    q = fp.fp4_fp8_quantize(x, sf_layout="mma")
+    row = fp.fp4_fp8_quantize(x)
+    for call in (lambda: fp.fp4_fp8_quantize(x.float()), lambda: fp.fp4_fp8_quantize(x.t()),
+                 lambda: fp.fp4_fp8_quantize(x, codes=torch.empty(4, 48, dtype=torch.uint8, device="cuda")),
+                 lambda: fp.fp4_fp8_quantize(x, scales=torch.empty(4, 2, dtype=torch.uint8, device="cuda")),
+                 lambda: fp.fp4_fp8_quantize(x, codes=torch.empty(4, 64, dtype=torch.uint8)),
+                 lambda: fp.fp4_fp8_gemm(q.codes, row.scales, q.codes, q.scales),
+                 lambda: fp.fp4_fp8_gemm(q.codes, q.scales, q.codes[:, :48], q.scales),
+                 lambda: fp.fp4_fp8_gemm(q.codes, q.scales, q.codes, q.scales.cpu()),
+                 lambda: fp.fp4_fp8_gemm(q.codes, q.scales, q.codes, q.scales, out=torch.empty(4, 5, device="cuda")),
+                 lambda: fp.fp4_fp8_gemm(q.codes.float(), q.scales, q.codes, q.scales),
+                 lambda: fp.fp4_fp8_dequantize(q.codes, q.scales)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(fp.Fp4Error):
+        fp.fp4_fp8_quantize(torch.zeros(4, 60, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(fp.Fp4Error):
+        fp.fp4_fp8_quantize(x[:0])
+    with pytest.raises(KeyError):
+        fp.fp4_fp8_quantize(x, "e3m4")
