@@ -653,9 +653,9 @@ fp4_status fp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int
   if (dresidual != nullptr && (s = check_rows16(dresidual, cols, lddr)) != FP4_OK) return s;
   if (!aligned16(dx) || !aligned16(dweight) || !aligned16(workspace)) return FP4_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(rstd) & 3u) != 0) return FP4_ERR_ALIGN;
-  int sms = 0;
-  if ((s = device_sms(&sms)) != FP4_OK) return s;
-  if (workspace_bytes < sizeof(float) * (size_t)cols * (size_t)rmsnorm_backward_parts(rows, cols, sms))
+  DeviceState* d = nullptr;
+  if ((s = device_state(&d)) != FP4_OK) return s;
+  if (workspace_bytes < sizeof(float) * (size_t)cols * (size_t)rmsnorm_backward_parts(rows, cols, d->num_sms))
     return FP4_ERR_ARG;
   RmsNormBackwardParams p;
   p.dy = dy;
@@ -672,7 +672,8 @@ fp4_status fp4_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int
   p.dx = dx;
   p.dweight = dweight;
   p.partials = static_cast<float*>(workspace);
-  return from_cuda(launch_rmsnorm_backward(p, sms, static_cast<cudaStream_t>(stream)));
+  p.error = d->scratch.error;
+  return from_cuda(launch_rmsnorm_backward(p, d->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fp4_fp8_scales_bytes(int64_t rows, int64_t cols, int axis, int sf_layout) {

@@ -55,6 +55,10 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0u;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // A: the 128 (or, over an SM pair, 256) rows of the accumulator; B: its n columns.  `id`: the byte of
 // the scale words that this block's instructions use.
 __device__ __forceinline__ uint32_t fp8_idesc(uint32_t m, uint32_t n, uint32_t a_type, uint32_t b_type, uint32_t id) {
@@ -132,6 +136,8 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
   const int kb0 = (int)((int64_t)nkb * rank / split), kb1 = (int)((int64_t)nkb * (rank + 1) / split);
 
   if (threadIdx.x == 0) {
+    prefetch_map(&tmap_w);
+    prefetch_map(&tmap_x);
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
@@ -486,6 +492,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
+    prefetch_map(&tmap_a);
+    prefetch_map(&tmap_b);
+    prefetch_map(&tmap_sa);
+    prefetch_map(&tmap_sb);
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);

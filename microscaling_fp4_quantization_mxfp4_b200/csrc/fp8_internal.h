@@ -86,6 +86,7 @@ struct RmsNormBackwardParams {
   void* dx;                     // bf16 [rows, cols] contiguous
   float* dweight;               // [cols]
   float* partials;              // [rmsnorm_backward_parts(...), cols]
+  unsigned* error;              // device error word
 };
 int rmsnorm_backward_parts(int64_t rows, int64_t cols, int num_sms);
 cudaError_t launch_rmsnorm_backward(const RmsNormBackwardParams& p, int num_sms, cudaStream_t st);

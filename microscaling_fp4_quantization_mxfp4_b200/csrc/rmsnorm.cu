@@ -32,6 +32,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
+__device__ __forceinline__ void unpack2(const uint4& v, float2 (&x)[4]) {
+  x[0] = make_float2(fp4dev::bf16_lo(v.x), fp4dev::bf16_hi(v.x));
+  x[1] = make_float2(fp4dev::bf16_lo(v.y), fp4dev::bf16_hi(v.y));
+  x[2] = make_float2(fp4dev::bf16_lo(v.z), fp4dev::bf16_hi(v.z));
+  x[3] = make_float2(fp4dev::bf16_lo(v.w), fp4dev::bf16_hi(v.w));
+}
 __device__ __forceinline__ void load_weight8(const void* w, int f32, uint32_t chunk, float (&v)[8]) {
   if (f32) {
     const float4 a = reinterpret_cast<const float4*>(w)[2 * chunk], b = reinterpret_cast<const float4*>(w)[2 * chunk + 1];
@@ -42,21 +48,19 @@ __device__ __forceinline__ void load_weight8(const void* w, int f32, uint32_t ch
   }
 }
 
-// Sum over the TPR threads of a row (every thread of the block takes part; `part` holds one float per
-// warp).  Warp shuffles, then the row's warps in order.
-template <int TPR, int THREADS>
-__device__ __forceinline__ float row_sum(float v, float* part) {
+// Sum over the `warps` warps of a row (every thread of the block takes part; `part` holds one float per
+// warp of the block).  Within the warp, then over the row's warps, in a fixed order.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* part, uint32_t first_warp, uint32_t warps) {
 #pragma unroll
-  for (int d = (TPR < 32 ? TPR : 32) / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  if (TPR > 32) {
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) part[warp] = v;
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  if (!WARP) {
+    const uint32_t lane = threadIdx.x & 31u;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    constexpr int W = TPR / 32;
-    const int w0 = warp / W * W;
-    v = part[w0];
+    v = lane < warps ? part[first_warp + lane] : 0.0f;
 #pragma unroll
-    for (int i = 1; i < W; ++i) v += part[w0 + i];
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
   }
   return v;
 }
@@ -73,25 +77,26 @@ struct NormArgs {
   uint16_t* norm_out;
   float* rstd;
   uint32_t cols, chunks, groups, main_ctas;
+  uint32_t tpr, slots;          // threads of a row (a multiple of 32), rows of a block
   int weight_f32, fmt, sf_mma;
 };
 
-// TPR threads a row, CPT 8-element chunks a thread: the row stays in registers between the sum of
+// tpr threads a row, CPT 8-element chunks a thread: the row stays in registers between the sum of
 // squares and the quantization, so x and the residual are read once.  Bound by HBM (7 bytes an element
-// with a residual); one row of few: by the latency of load -> sum -> store.
-template <int TPR, int CPT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_fp8_kernel(NormArgs p) {
-  constexpr int kThreads = TPR < 256 ? 256 : TPR;
-  constexpr int kRows = kThreads / TPR;
-  __shared__ float part[kThreads / 32];
+// with a residual); one row of few: by the latency of load -> sum -> store.  WARP: a row is one warp's,
+// and nothing waits for another warp.
+template <int CPT, bool WARP>
+__global__ void __launch_bounds__(CPT == 1 || CPT == 2 ? 1024 : 512) rmsnorm_fp8_kernel(NormArgs p) {
+  __shared__ float part[32];
   pdl_trigger();
+  const uint32_t TPR = WARP ? 32u : p.tpr;
+  const uint32_t slot = WARP ? threadIdx.x >> 5 : threadIdx.x / TPR, t = threadIdx.x - slot * TPR;
   pdl_wait();
   if (blockIdx.x >= p.main_ctas) {
     zero_pad_rows(p.scales, p.rows, p.groups);
     return;
   }
-  const uint32_t t = threadIdx.x % TPR;
-  const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
+  const long long row = (long long)blockIdx.x * p.slots + slot;
   const bool live = row < p.rows;
   uint4 h[CPT];
 #pragma unroll
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_fp8_kernel(Norm
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = __fmaf_rn(a[i], a[i], ss);
   }
-  ss = row_sum<TPR, kThreads>(ss, part);
+  ss = row_sum<WARP>(ss, part, slot * (TPR / 32), TPR / 32);
   const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, p.fcols), p.eps));
   if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
 #pragma unroll
@@ -173,92 +178,275 @@ struct NormBwdArgs {
   uint16_t* dx;
   float* partials;
   long long rows, lddy, ldh, lddr;
-  float fcols;
-  uint32_t cols, chunks;
+  float inv_cols;
+  uint32_t cols, chunks, tpr, slots;
   int weight_f32;
 };
 
-// Every CTA walks rows blockIdx, blockIdx + gridDim, ... (kRows of them at a time) and keeps its
-// columns' sums of dy * xh in registers; they leave once, as one row of `partials` per row slot.
-template <int TPR, int CPT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_backward_kernel(NormBwdArgs p) {
-  constexpr int kThreads = TPR < 256 ? 256 : TPR;
-  constexpr int kRows = kThreads / TPR;
-  __shared__ float part[2][kThreads / 32];
+// Writes the block's row of `partials`: eight columns of each chunk.
+template <int CPT>
+__device__ __forceinline__ void store_partials(const NormBwdArgs& p, const float2 (&acc)[CPT][4], uint32_t t, uint32_t tpr) {
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+    if (t + k * tpr < p.chunks) {
+      float* o = p.partials + (long long)blockIdx.x * p.cols + (t + k * tpr) * 8;
+      reinterpret_cast<float4*>(o)[0] = make_float4(acc[k][0].x, acc[k][0].y, acc[k][1].x, acc[k][1].y);
+      reinterpret_cast<float4*>(o)[1] = make_float4(acc[k][2].x, acc[k][2].y, acc[k][3].x, acc[k][3].y);
+    }
+}
+
+// Rows of up to 1024 elements: a warp a row, eight rows a block.  A warp walks its rows with the next one's
+// loads issued before this one's sum and keeps its columns' sums of dy * xh in registers.
+template <int CPT>
+__global__ void __launch_bounds__(256, 2) rmsnorm_backward_short_kernel(NormBwdArgs p) {
+  extern __shared__ float2 slot_sums[];             // [7][4][chunks]
   pdl_trigger();
-  pdl_wait();
-  const uint32_t t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
-  float acc[CPT][8];
+  const uint32_t slot = threadIdx.x >> 5, t = threadIdx.x & 31u;
+  const long long step = (long long)gridDim.x * p.slots;
+  float2 acc[CPT][4];
 #pragma unroll
   for (int k = 0; k < CPT; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[k][i] = 0.0f;
-  int flip = 0;
-  for (long long r0 = (long long)blockIdx.x * kRows; r0 < p.rows; r0 += (long long)gridDim.x * kRows, flip ^= 1) {
-    const long long row = r0 + slot;
+    for (int i = 0; i < 4; ++i) acc[k][i] = make_float2(0.0f, 0.0f);
+  pdl_wait();
+  uint4 nd[CPT], nh[CPT];
+  float nrstd = 0.0f;
+  auto load = [&](long long row) {
     const bool live = row < p.rows;
-    const float rstd = live ? p.rstd[row] : 0.0f;
-    uint4 d[CPT], h[CPT];
-    float s = 0.0f;
+    nrstd = live ? p.rstd[row] : 0.0f;
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-      const uint32_t c = t + k * TPR;
-      d[k] = h[k] = make_uint4(0, 0, 0, 0);
+      const uint32_t c = t + k * 32;
+      nd[k] = nh[k] = make_uint4(0, 0, 0, 0);
       if (live && c < p.chunks) {
-        d[k] = *reinterpret_cast<const uint4*>(p.dy + row * p.lddy + c * 8);
-        h[k] = *reinterpret_cast<const uint4*>(p.h + row * p.ldh + c * 8);
+        nd[k] = *reinterpret_cast<const uint4*>(p.dy + row * p.lddy + c * 8);
+        nh[k] = *reinterpret_cast<const uint4*>(p.h + row * p.ldh + c * 8);
       }
     }
+  };
+  long long row = (long long)blockIdx.x * p.slots + slot;
+  load(row);
+  for (; row < p.rows; row += step) {
+    const float2 r2 = make_float2(nrstd, nrstd);
+    uint4 d[CPT], h[CPT], r4[CPT];
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-      const uint32_t c = t + k * TPR;
-      if (live && c < p.chunks) {
-        float a[8], b[8], w[8];
-        fp4dev::unpack8(d[k], a);
-        fp4dev::unpack8(h[k], b);
+      const uint32_t c = t + k * 32;
+      d[k] = nd[k];
+      h[k] = nh[k];
+      r4[k] = make_uint4(0, 0, 0, 0);
+      if (p.dres != nullptr && c < p.chunks) r4[k] = *reinterpret_cast<const uint4*>(p.dres + row * p.lddr + c * 8);
+    }
+    load(row + step);
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) {
+      const uint32_t c = t + k * 32;
+      if (c < p.chunks) {
+        float2 a[4], b[4];
+        float w[8];
+        unpack2(d[k], a);
+        unpack2(h[k], b);
         load_weight8(p.weight, p.weight_f32, c, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float xh = __fmul_rn(b[i], rstd);
-          s = __fmaf_rn(__fmul_rn(a[i], w[i]), xh, s);
-          acc[k][i] = __fmaf_rn(a[i], xh, acc[k][i]);
+        for (int i = 0; i < 4; ++i) {
+          const float2 xh = __fmul2_rn(b[i], r2);
+          s2 = __ffma2_rn(__fmul2_rn(a[i], make_float2(w[2 * i], w[2 * i + 1])), xh, s2);
+          acc[k][i] = __ffma2_rn(a[i], xh, acc[k][i]);
         }
       }
     }
-    s = row_sum<TPR, kThreads>(s, part[flip]);       // two buffers: one barrier a row
-    const float c1 = __fdiv_rn(s, p.fcols);
+    const float sum = row_sum<true>(__fadd_rn(s2.x, s2.y), nullptr, 0, 1);
+    // dx = g * rstd + (h * (-rstd^2 * c) + dresidual)
+    const float kf = __fmul_rn(__fmul_rn(-r2.x, r2.x), __fmul_rn(sum, p.inv_cols));
+    const float2 k2 = make_float2(kf, kf);
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-      const uint32_t c = t + k * TPR;
-      if (live && c < p.chunks) {
-        float a[8], b[8], w[8], r[8];
-        fp4dev::unpack8(d[k], a);
-        fp4dev::unpack8(h[k], b);
+      const uint32_t c = t + k * 32;
+      if (c < p.chunks) {
+        float2 a[4], b[4], e[4];
+        float w[8];
+        unpack2(d[k], a);
+        unpack2(h[k], b);
+        unpack2(r4[k], e);
         load_weight8(p.weight, p.weight_f32, c, w);
-        if (p.dres != nullptr) {
-          fp4dev::unpack8(*reinterpret_cast<const uint4*>(p.dres + row * p.lddr + c * 8), r);
-        } else {
+        uint32_t o[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = __ffma2_rn(__fmul2_rn(a[i], make_float2(w[2 * i], w[2 * i + 1])), r2, __ffma2_rn(b[i], k2, e[i]));
+          o[i] = pack_bf16(v.x, v.y);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float g = __fmul_rn(a[i], w[i]), xh = __fmul_rn(b[i], rstd);
-          a[i] = __fmaf_rn(rstd, __fmaf_rn(-xh, c1, g), r[i]);
-        }
-        *reinterpret_cast<uint4*>(p.dx + row * p.cols + c * 8) = pack8(a);
+        *reinterpret_cast<uint4*>(p.dx + row * p.cols + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
-  float* out = p.partials + ((long long)blockIdx.x * kRows + slot) * p.cols;
+  // the eight warps' sums, in order
 #pragma unroll
-  for (int k = 0; k < CPT; ++k) {
-    const uint32_t c = t + k * TPR;
-    if (c < p.chunks) {
-      reinterpret_cast<float4*>(out + c * 8)[0] = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
-      reinterpret_cast<float4*>(out + c * 8)[1] = make_float4(acc[k][4], acc[k][5], acc[k][6], acc[k][7]);
+  for (int k = 0; k < CPT; ++k)
+    if (slot > 0 && t + k * 32 < p.chunks)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) slot_sums[((slot - 1) * 4 + i) * p.chunks + t + k * 32] = acc[k][i];
+  __syncthreads();
+  if (slot > 0) return;
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+    if (t + k * 32 < p.chunks)
+      for (uint32_t j = 0; j + 1 < p.slots; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[k][i] = fp4dev::add2(acc[k][i], slot_sums[(j * 4 + i) * p.chunks + t + k * 32]);
+  store_partials<CPT>(p, acc, t, 32);
+}
+
+// Longer rows: a block takes R rows at a time, CPT chunks a thread.  Rows arrive in a ring of shared-memory
+// slots by bulk copies (one an array), so that what is in flight takes no registers, and are read from there
+// twice, for the sum and for dx.  The sums of R rows share one barrier; behind it every thread has read the
+// previous R rows, and their slots are filled again.  What a row costs a thread besides its elements (waits,
+// shuffles, addresses: some 60 instructions) is why a thread takes 16 elements of it and not 8, and the
+// arithmetic runs on packed pairs.
+template <int R>
+__global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs p, int ring_rows, unsigned* error) {
+  constexpr int CPT = 2;
+  extern __shared__ __align__(128) uint8_t ring[];              // [ring_rows][arrays][cols] bf16, then the barriers
+  __shared__ float part[2][R][32];
+  pdl_trigger();
+  const uint32_t t = threadIdx.x, TPR = p.tpr, warp = t >> 5, lane = t & 31u, warps = TPR / 32;
+  const uint32_t row_bytes = p.cols * 2, arrays = p.dres != nullptr ? 3 : 2, slot_bytes = row_bytes * arrays;
+  const uint32_t ring0 = fp4dev::smem_addr(ring), bar0 = ring0 + (uint32_t)ring_rows * slot_bytes;
+  if (t == 0) {
+    for (int s = 0; s < ring_rows; ++s) fp4dev::mbar_init(bar0 + 8 * s, 1);
+    fp4dev::mbar_init_fence();
+  }
+  float2 acc[CPT][4], w[CPT][4];
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[k][i] = w[k][i] = make_float2(0.0f, 0.0f);
+  pdl_wait();
+  __syncthreads();
+  const int count = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);      // rows blockIdx + n * gridDim
+  int fetched = 0, fetch_slot = 0;                             // thread 0: rows asked for, the next one's slot
+  long long fetch_row = blockIdx.x;
+  auto fetch = [&] {
+    const uint32_t bar = bar0 + 8 * fetch_slot, dst = ring0 + (uint32_t)fetch_slot * slot_bytes;
+    fp4dev::mbar_expect_tx(bar, slot_bytes);
+    fp4dev::bulk_g2s(dst, p.dy + fetch_row * p.lddy, row_bytes, bar);
+    fp4dev::bulk_g2s(dst + row_bytes, p.h + fetch_row * p.ldh, row_bytes, bar);
+    if (arrays == 3) fp4dev::bulk_g2s(dst + 2 * row_bytes, p.dres + fetch_row * p.lddr, row_bytes, bar);
+    ++fetched;
+    fetch_row += gridDim.x;
+    if (++fetch_slot == ring_rows) fetch_slot = 0;
+  };
+  if (t == 0)
+    while (fetched < ring_rows && fetched < count) fetch();
+#pragma unroll
+  for (int k = 0; k < CPT; ++k)
+    if (t + k * TPR < p.chunks) {
+      float v[8];
+      load_weight8(p.weight, p.weight_f32, t + k * TPR, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[k][i] = make_float2(v[2 * i], v[2 * i + 1]);
+    }
+  const float* rs = p.rstd + blockIdx.x;
+  uint16_t* out = p.dx + (long long)blockIdx.x * p.cols + t * 8;
+  const long long out_step = (long long)gridDim.x * p.cols;
+  float nrstd[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) nrstd[r] = r < count ? rs[(long long)r * gridDim.x] : 0.0f;
+  bool late = false;
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int n0 = 0, flip = 0; n0 < count; n0 += R, flip ^= 1) {
+    float rstd[R], sum[R];
+    uint32_t at[R];                                            // the rows' slots
+    rs += (long long)R * gridDim.x;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rstd[r] = nrstd[r];
+      nrstd[r] = n0 + R + r < count ? rs[(long long)r * gridDim.x] : 0.0f;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sum[r] = 0.0f;
+      at[r] = (uint32_t)slot * slot_bytes + t * 16;
+      if (n0 + r < count) {
+        if (!late && !fp4dev::mbar_wait_bounded(bar0 + 8 * slot, phase)) {
+          late = true;                                         // reported; the remaining waits are skipped
+          atomicOr(error, 1u);
+        }
+        if (++slot == ring_rows) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        const float2 r2 = make_float2(rstd[r], rstd[r]);
+        float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+          if (t + k * TPR < p.chunks) {
+            float2 a[4], b[4];
+            unpack2(*reinterpret_cast<const uint4*>(ring + at[r] + k * TPR * 16), a);
+            unpack2(*reinterpret_cast<const uint4*>(ring + at[r] + row_bytes + k * TPR * 16), b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 xh = __fmul2_rn(b[i], r2);
+              s2 = __ffma2_rn(__fmul2_rn(a[i], w[k][i]), xh, s2);
+              acc[k][i] = __ffma2_rn(a[i], xh, acc[k][i]);
+            }
+          }
+        }
+        sum[r] = __fadd_rn(s2.x, s2.y);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], d);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (lane == 0) part[flip][r][warp] = sum[r];
+    __syncthreads();                                           // one barrier for R rows: two sets of sums
+    if (t == 0 && n0 > 0)
+      for (int r = 0; r < R && fetched < count; ++r) fetch();
+#pragma unroll
+    for (int r = 0; r < R; ++r) sum[r] = lane < warps ? part[flip][r][lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], d);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (n0 + r < count) {
+        // dx = g * rstd + (h * (-rstd^2 * c) + dresidual)
+        const float kf = __fmul_rn(__fmul_rn(-rstd[r], rstd[r]), __fmul_rn(sum[r], p.inv_cols));
+        const float2 r2 = make_float2(rstd[r], rstd[r]), k2 = make_float2(kf, kf);
+#pragma unroll
+        for (int k = 0; k < CPT; ++k) {
+          if (t + k * TPR < p.chunks) {
+            float2 a[4], b[4], e[4];
+            unpack2(*reinterpret_cast<const uint4*>(ring + at[r] + k * TPR * 16), a);
+            unpack2(*reinterpret_cast<const uint4*>(ring + at[r] + row_bytes + k * TPR * 16), b);
+            if (arrays == 3) {
+              unpack2(*reinterpret_cast<const uint4*>(ring + at[r] + 2 * row_bytes + k * TPR * 16), e);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[i] = make_float2(0.0f, 0.0f);
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 v = __ffma2_rn(__fmul2_rn(a[i], w[k][i]), r2, __ffma2_rn(b[i], k2, e[i]));
+              o[i] = pack_bf16(v.x, v.y);
+            }
+            *reinterpret_cast<uint4*>(out + k * TPR * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        out += out_step;
+      }
     }
   }
+  if (late && t == 0)                                          // no copy may land after the block has gone
+    for (int n = fetched > ring_rows ? fetched - ring_rows : 0; n < fetched; ++n)
+      fp4dev::mbar_wait_bounded(bar0 + 8 * (n % ring_rows), (uint32_t)(n / ring_rows) & 1u);
+  store_partials<CPT>(p, acc, t, TPR);
 }
 
 // dweight[c] = sum over the partials' rows, in a fixed order: 32 columns a CTA, 32 rows at a time.
@@ -269,8 +457,10 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* partials,
   pdl_wait();
   const uint32_t x = threadIdx.x & 31u, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
   float v = 0.0f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 8
     for (uint32_t r = y; r < parts; r += 32) v = __fadd_rn(v, partials[(long long)r * cols + c]);
+  }
   s[y][x] = v;
   __syncthreads();
   v = s[x][y];
@@ -279,35 +469,43 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* partials,
   if (x == 0 && blockIdx.x * 32 + y < cols) out[blockIdx.x * 32 + y] = v;
 }
 
-// Threads a row: the least power of two with at most `cpt` chunks a thread.
-int threads_for(int64_t chunks, int cpt, int most) {
-  int t = 32;
-  while (t < most && (int64_t)t * cpt < chunks) t *= 2;
-  return t;
+// How a row is spread: chunks a thread, threads a row (a multiple of 32), rows a block.
+struct RowShape {
+  int cpt;
+  uint32_t tpr, slots;
+};
+// Rows of up to 128 chunks (1024 elements) are a warp's own; longer ones take four chunks a thread, in blocks
+// of at least 128 threads.
+RowShape row_shape(int64_t chunks) {
+  if (chunks <= 128) return {(int)((chunks + 31) / 32), 32u, 8u};
+  const uint32_t tpr = (uint32_t)((chunks + 127) / 128 * 32);
+  return {4, tpr, tpr >= 128 ? 1u : 256u / tpr};
 }
 
-template <int TPR, int CPT>
-cudaError_t run_norm(const NormArgs& a, cudaStream_t st) {
-  constexpr int kThreads = TPR < 256 ? 256 : TPR;
-  NormArgs p = a;
-  p.main_ctas = (uint32_t)((a.rows + kThreads / TPR - 1) / (kThreads / TPR));
-  const uint32_t grid = p.main_ctas + (a.sf_mma && a.rows % 128 != 0 ? 1u : 0u);
-  return launch_kernel(rmsnorm_fp8_kernel<TPR, CPT>, dim3(grid), dim3(kThreads), 0, st, false, 1u, p);
+template <int CPT, bool WARP>
+cudaError_t run_norm(const NormArgs& p, uint32_t grid, cudaStream_t st) {
+  return launch_kernel(rmsnorm_fp8_kernel<CPT, WARP>, dim3(grid), dim3(p.tpr * p.slots), 0, st, false, 1u, p);
 }
 
-// Chunks a thread of the backward kernel, and the threads of a row that follow from it.
-constexpr int kBwdChunks = 2;
-void backward_shape(int64_t cols, int* tpr, int* cpt) {
-  const int64_t chunks = cols / 8;
-  *tpr = threads_for(chunks, kBwdChunks, 512);
-  *cpt = (int64_t)*tpr * kBwdChunks >= chunks ? kBwdChunks : 4;
+template <int CPT>
+cudaError_t run_short(const NormBwdArgs& p, int parts, cudaStream_t st) {
+  return launch_kernel(rmsnorm_backward_short_kernel<CPT>, dim3(parts), dim3(256), (p.slots - 1) * p.cols * sizeof(float),
+                       st, false, 1u, p);
 }
 
-template <int TPR, int CPT>
-cudaError_t run_backward(const NormBwdArgs& p, int parts, cudaStream_t st) {
-  constexpr int kThreads = TPR < 256 ? 256 : TPR;
-  return launch_kernel(rmsnorm_backward_kernel<TPR, CPT>, dim3(parts / (kThreads / TPR)), dim3(kThreads), 0, st, false,
-                       1u, p);
+// The long rows' ring: two blocks an SM where each holds four rows of three arrays, else one.
+constexpr int64_t kRingBytes = 222 * 1024;
+int long_blocks(int64_t cols) { return 4 * cols * 6 <= kRingBytes / 2 ? 2 : 1; }
+
+template <int R>
+cudaError_t run_long(const NormBwdArgs& p, int parts, unsigned* error, cudaStream_t st) {
+  auto kernel = rmsnorm_backward_long_kernel<R>;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes + 256);
+  if (attr != cudaSuccess) return attr;
+  const int64_t slot = (int64_t)p.cols * 2 * (p.dres != nullptr ? 3 : 2);
+  const int rows = (int)std::min<int64_t>(16, kRingBytes / long_blocks(p.cols) / slot);
+  return launch_kernel(kernel, dim3(parts), dim3(p.tpr), (size_t)(rows * (slot + 8)), st, false, 1u, p, rows, error);
 }
 
 }  // namespace
@@ -335,36 +533,36 @@ cudaError_t launch_rmsnorm_fp8(const RmsNormParams& q, int num_sms, cudaStream_t
   p.weight_f32 = q.weight_f32;
   p.fmt = q.fmt;
   p.sf_mma = q.sf_mma;
-  // With a row for every SM the rows hide each other's latency and two chunks a thread move more bytes
-  // per instruction; with fewer rows than SMs the row itself is spread over as many threads as it has chunks.
-  const int cpt = q.rows < num_sms ? 1 : 2;
-  const int tpr = threads_for(p.chunks, cpt, 1024);
-  if (cpt == 1 && (int64_t)tpr >= p.chunks) {
-    switch (tpr) {
-      case 32: return run_norm<32, 1>(p, st);
-      case 64: return run_norm<64, 1>(p, st);
-      case 128: return run_norm<128, 1>(p, st);
-      case 256: return run_norm<256, 1>(p, st);
-      case 512: return run_norm<512, 1>(p, st);
-      default: return run_norm<1024, 1>(p, st);
+  // With fewer rows than SMs nothing hides a row's latency but its own width: as many threads as it has chunks.
+  RowShape shape = row_shape(p.chunks);
+  if (q.rows < num_sms) {
+    const int cpt = p.chunks <= 1024 ? 1 : 2;
+    shape = {cpt, (p.chunks + 32 * cpt - 1) / (32 * cpt) * 32, 1u};
+  }
+  p.tpr = shape.tpr;
+  p.slots = shape.slots;
+  p.main_ctas = (uint32_t)((q.rows + shape.slots - 1) / shape.slots);
+  const uint32_t grid = p.main_ctas + (p.sf_mma && q.rows % 128 != 0 ? 1u : 0u);
+  if (shape.tpr == 32) {
+    switch (shape.cpt) {
+      case 1: return run_norm<1, true>(p, grid, st);
+      case 2: return run_norm<2, true>(p, grid, st);
+      case 3: return run_norm<3, true>(p, grid, st);
+      default: return run_norm<4, true>(p, grid, st);
     }
   }
-  switch (tpr) {
-    case 32: return run_norm<32, 2>(p, st);
-    case 64: return run_norm<64, 2>(p, st);
-    case 128: return run_norm<128, 2>(p, st);
-    case 256: return run_norm<256, 2>(p, st);
-    case 512: return run_norm<512, 2>(p, st);
-    default: return run_norm<1024, 2>(p, st);
+  switch (shape.cpt) {
+    case 1: return run_norm<1, false>(p, grid, st);
+    case 2: return run_norm<2, false>(p, grid, st);
+    default: return run_norm<4, false>(p, grid, st);
   }
 }
 
+// Blocks of the backward kernel, each a row of partial sums.
 int rmsnorm_backward_parts(int64_t rows, int64_t cols, int num_sms) {
-  int tpr, cpt;
-  backward_shape(cols, &tpr, &cpt);
-  const int threads = tpr < 256 ? 256 : tpr, slots = threads / tpr;
-  const int64_t most = (int64_t)num_sms * (1024 / threads);           // CTAs that fill the device
-  return (int)std::min<int64_t>(most, (rows + slots - 1) / slots) * slots;
+  const int64_t slots = cols <= 1024 ? 8 : 1;
+  const int64_t most = (int64_t)num_sms * (cols <= 1024 ? 2 : long_blocks(cols));
+  return (int)std::min<int64_t>(most, (rows + slots - 1) / slots);
 }
 
 cudaError_t launch_rmsnorm_backward(const RmsNormBackwardParams& q, int num_sms, cudaStream_t st) {
@@ -380,20 +578,26 @@ cudaError_t launch_rmsnorm_backward(const RmsNormBackwardParams& q, int num_sms,
   p.lddy = q.lddy;
   p.ldh = q.ldh;
   p.lddr = q.lddr;
-  p.fcols = (float)q.cols;
+  p.inv_cols = 1.0f / (float)q.cols;
   p.cols = (uint32_t)q.cols;
   p.chunks = (uint32_t)(q.cols / 8);
   p.weight_f32 = q.weight_f32;
   const int parts = rmsnorm_backward_parts(q.rows, q.cols, num_sms);
-  int tpr, cpt;
-  backward_shape(q.cols, &tpr, &cpt);
   cudaError_t e;
-  switch (tpr) {
-    case 32: e = run_backward<32, 2>(p, parts, st); break;
-    case 64: e = run_backward<64, 2>(p, parts, st); break;
-    case 128: e = run_backward<128, 2>(p, parts, st); break;
-    case 256: e = run_backward<256, 2>(p, parts, st); break;
-    default: e = cpt == 2 ? run_backward<512, 2>(p, parts, st) : run_backward<512, 4>(p, parts, st); break;
+  if (p.chunks <= 128) {
+    p.tpr = 32;
+    p.slots = 8;
+    switch ((p.chunks + 31) / 32) {
+      case 1: e = run_short<1>(p, parts, st); break;
+      case 2: e = run_short<2>(p, parts, st); break;
+      case 3: e = run_short<3>(p, parts, st); break;
+      default: e = run_short<4>(p, parts, st); break;
+    }
+  } else {
+    p.tpr = (p.chunks + 63) / 64 * 32;
+    p.slots = 1;
+    // two rows a barrier where the ring holds eight of them
+    e = 8 * (int64_t)p.cols * 6 <= kRingBytes / 2 ? run_long<2>(p, parts, q.error, st) : run_long<1>(p, parts, q.error, st);
   }
   if (e != cudaSuccess) return e;
   return launch_kernel(column_sum_kernel, dim3((p.cols + 31) / 32), dim3(1024), 0, st, false, 1u,
