@@ -17,9 +17,9 @@ namespace {
 using namespace fp8dev;
 
 // ------------------------------------------------------- blocks along rows --
-// Half a warp per block: 16 lanes x 8 elements (one 16-byte load each), the block's maximum by four
-// shuffles, 8-byte code stores (128 contiguous bytes a block).  Bound by HBM: 2 bytes in, 1 out per
-// element.  Each warp takes kUnroll pairs of adjacent blocks with all loads in flight at once.
+// Half a warp per block: 16 lanes x 8 elements (one 16-byte load each), 8-byte code stores (128 contiguous
+// bytes a block).  Bound by HBM: 2 bytes in, 1 out per element.  Each warp takes kUnroll pairs of adjacent
+// blocks with all loads in flight at once.
 constexpr int kRowThreads = 256;
 constexpr int kUnroll = 4;
 
@@ -44,34 +44,54 @@ __global__ void __launch_bounds__(kRowThreads) fp8_quantize_rows_kernel(RowArgs 
   }
   const uint32_t lane = threadIdx.x & 31u, half = lane >> 4, c16 = lane & 15u;
   const uint32_t warp = (blockIdx.x * kRowThreads + threadIdx.x) >> 5;
-  const uint32_t first = warp * (2 * kUnroll);
+  const uint32_t first = warp * (2 * kUnroll) + half;               // blocks first, first + 2, ... in row order
   uint4 v[kUnroll];
   uint32_t row[kUnroll], g[kUnroll];
   bool on[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t it = first + 2 * u + half;
-    row[u] = it / p.groups;
-    g[u] = it - row[u] * p.groups;
-    on[u] = it < p.items && g[u] * 16 + c16 < p.chunks;
+    if (u == 0) {
+      row[0] = first / p.groups;
+      g[0] = first - row[0] * p.groups;
+    } else {
+      row[u] = row[u - 1];
+      g[u] = g[u - 1] + 2;
+      while (g[u] >= p.groups) {
+        g[u] -= p.groups;
+        ++row[u];
+      }
+    }
+    on[u] = first + 2 * u < p.items && g[u] * 16 + c16 < p.chunks;
     v[u] = make_uint4(0, 0, 0, 0);
     if (on[u]) v[u] = *reinterpret_cast<const uint4*>(p.x + (long long)row[u] * p.ld + (g[u] * 16 + c16) * 8);
   }
+  uint32_t m[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) m[u] = pair_bits(max_abs8(v[u]));
+  float inv[kUnroll];
+  int own;
+  bool stores;
+  const uint32_t byte = block_scales<FMT>(m, inv, own, stores);
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t byte = scale_byte<FMT>(max_half_warp(pair_bits(max_abs8(v[u]))));
-    const float inv = inv_scale(byte);
-    float e[8];
-    fp4dev::unpack8(v[u], e);
-    if (on[u])
-      *reinterpret_cast<uint2*>(p.codes + (long long)row[u] * p.ldc + (g[u] * 16 + c16) * 8) = codes8<FMT>(e, inv);
-    if (first + 2 * u + half < p.items) {
-      if (c16 == 0) {
-        p.scales[sf_offset(p.sf_mma, row[u], g[u], p.groups)] = (uint8_t)byte;
-      } else if (p.sf_mma && g[u] + 1 == p.groups && c16 <= ((4u - (p.groups & 3u)) & 3u)) {
-        p.scales[sf_offset(1, row[u], g[u] + c16, p.groups)] = 0;       // groups that pad the layout to 4
-      }
+    if (on[u]) {
+      float2 e[4];
+      unpack2(v[u], e);
+      *reinterpret_cast<uint2*>(p.codes + (long long)row[u] * p.ldc + (g[u] * 16 + c16) * 8) = codes8<FMT>(e, inv[u]);
     }
+  }
+  if (stores && first + 2 * own < p.items) {
+    uint32_t r = row[0], b = g[0];
+#pragma unroll
+    for (int u = 1; u < kUnroll; ++u)
+      if (own == u) {
+        r = row[u];
+        b = g[u];
+      }
+    uint8_t* out = p.scales + sf_offset(p.sf_mma, r, b, p.groups);
+    *out = (uint8_t)byte;
+    if (p.sf_mma && b + 1 == p.groups)                              // groups that pad the layout to 4
+      for (uint32_t k = 1; (b + k) & 3u; ++k) out[k] = 0;
   }
 }
 
@@ -157,8 +177,8 @@ __global__ void __launch_bounds__(kTileThreads) fp8_quantize_tile_kernel(TileArg
     for (int i = 0; i < kTileLoads; ++i) {
       const int r = (t >> 4) + 16 * i, c = (t & 15) * 8;
       if (r0 + r < p.rows && c0 + c < p.cols) {
-        float e[8];
-        fp4dev::unpack8(v[i], e);
+        float2 e[4];
+        unpack2(v[i], e);
         *reinterpret_cast<uint2*>(p.codes + (r0 + r) * p.ldc + c0 + c) = codes8<FMT>(e, inv);
       }
     }

@@ -52,9 +52,17 @@ __device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
 }
 // Eight elements times `inv` -> eight codes.
 template <int FMT>
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
-  return make_uint2(cvt4<FMT>(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv), __fmul_rn(v[2], inv), __fmul_rn(v[3], inv)),
-                    cvt4<FMT>(__fmul_rn(v[4], inv), __fmul_rn(v[5], inv), __fmul_rn(v[6], inv), __fmul_rn(v[7], inv)));
+__device__ __forceinline__ uint2 codes8(const float2 (&v)[4], float inv) {
+  const float2 s = make_float2(inv, inv);
+  const float2 a = __fmul2_rn(v[0], s), b = __fmul2_rn(v[1], s), c = __fmul2_rn(v[2], s), d = __fmul2_rn(v[3], s);
+  return make_uint2(cvt4<FMT>(a.x, a.y, b.x, b.y), cvt4<FMT>(c.x, c.y, d.x, d.y));
+}
+// Eight bf16 elements as fp32 pairs.
+__device__ __forceinline__ void unpack2(const uint4& v, float2 (&x)[4]) {
+  x[0] = make_float2(fp4dev::bf16_lo(v.x), fp4dev::bf16_hi(v.x));
+  x[1] = make_float2(fp4dev::bf16_lo(v.y), fp4dev::bf16_hi(v.y));
+  x[2] = make_float2(fp4dev::bf16_lo(v.z), fp4dev::bf16_hi(v.z));
+  x[3] = make_float2(fp4dev::bf16_lo(v.w), fp4dev::bf16_hi(v.w));
 }
 
 // Two bf16 magnitudes at once: the larger of each half, as 16-bit patterns.
@@ -65,11 +73,53 @@ __device__ __forceinline__ uint32_t max_abs8(const uint4& v) {
 // Larger half of a 16-bit pair as an fp32 bit pattern.
 __device__ __forceinline__ uint32_t pair_bits(uint32_t m) { return max(m << 16, m & 0xFFFF0000u); }
 
-// Largest value over the 16 lanes that hold one block (half a warp; all 32 lanes take part).
-__device__ __forceinline__ uint32_t max_half_warp(uint32_t v) {
+// Larger magnitude of three, NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Scale bytes of the N (at most 4) blocks that each half warp holds, 8 elements a lane and block: m[j] is
+// the lane's part of block j's maximum.  The butterfly halves the blocks with the lanes, so that four maxima
+// take five shuffles instead of sixteen and each lane works out one byte, that of block `own` (which may be N
+// or more: no block); four more hand out the inverse scales.  `first`: the lane that stores the byte.
+template <int FMT, int N>
+__device__ __forceinline__ uint32_t block_scales(const uint32_t (&m)[N], float (&inv)[N], int& own, bool& first) {
+  const int lane = threadIdx.x & 31;
+  uint32_t k;
+  if (N == 1) {
+    k = m[0];
+    k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 8));
+    k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 4));
+    own = 0;
+    first = (lane & 15) == 0;
+  } else if (N == 2) {
+    const bool b = (lane & 8) != 0;
+    k = max(b ? m[1 % N] : m[0], __shfl_xor_sync(0xFFFFFFFFu, b ? m[0] : m[1 % N], 8));
+    k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 4));
+    own = b ? 1 : 0;
+    first = (lane & 7) == 0;
+  } else {
+    const bool b = (lane & 8) != 0, c = (lane & 4) != 0;
+    const uint32_t m3 = N == 4 ? m[N - 1] : 0u;
+    const uint32_t k0 = max(b ? m[2 % N] : m[0], __shfl_xor_sync(0xFFFFFFFFu, b ? m[0] : m[2 % N], 8));
+    const uint32_t k1 = max(b ? m3 : m[1 % N], __shfl_xor_sync(0xFFFFFFFFu, b ? m[1 % N] : m3, 8));
+    k = max(c ? k1 : k0, __shfl_xor_sync(0xFFFFFFFFu, c ? k0 : k1, 4));
+    own = (lane >> 2) & 3;
+    first = (lane & 3) == 0;
+  }
+  k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 2));
+  k = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 1));
+  const uint32_t byte = scale_byte<FMT>(k);
+  const float mine = inv_scale(byte);
+  if (N == 1) {
+    inv[0] = mine;
+  } else {
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-  return v;
+    for (int j = 0; j < N; ++j) inv[j] = __shfl_sync(0xFFFFFFFFu, mine, (lane & 16) | (j * (N == 2 ? 8 : 4)));
+  }
+  return byte;
 }
 
 __device__ __forceinline__ long long sf_offset(int sf_mma, long long row, long long g, long long groups) {

@@ -29,15 +29,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)) |
          ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16);
 }
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-__device__ __forceinline__ void unpack2(const uint4& v, float2 (&x)[4]) {
-  x[0] = make_float2(fp4dev::bf16_lo(v.x), fp4dev::bf16_hi(v.x));
-  x[1] = make_float2(fp4dev::bf16_lo(v.y), fp4dev::bf16_hi(v.y));
-  x[2] = make_float2(fp4dev::bf16_lo(v.z), fp4dev::bf16_hi(v.z));
-  x[3] = make_float2(fp4dev::bf16_lo(v.w), fp4dev::bf16_hi(v.w));
-}
 __device__ __forceinline__ void load_weight8(const void* w, int f32, uint32_t chunk, float (&v)[8]) {
   if (f32) {
     const float4 a = reinterpret_cast<const float4*>(w)[2 * chunk], b = reinterpret_cast<const float4*>(w)[2 * chunk + 1];
@@ -78,14 +69,14 @@ struct NormArgs {
   float* rstd;
   uint32_t cols, chunks, groups, main_ctas;
   uint32_t tpr, slots;          // threads of a row (a multiple of 32), rows of a block
-  int weight_f32, fmt, sf_mma;
+  int weight_f32, sf_mma;
 };
 
 // tpr threads a row, CPT 8-element chunks a thread: the row stays in registers between the sum of
 // squares and the quantization, so x and the residual are read once.  Bound by HBM (7 bytes an element
 // with a residual); one row of few: by the latency of load -> sum -> store.  WARP: a row is one warp's,
 // and nothing waits for another warp.
-template <int CPT, bool WARP>
+template <int FMT, int CPT, bool WARP>
 __global__ void __launch_bounds__(CPT == 1 || CPT == 2 ? 1024 : 512) rmsnorm_fp8_kernel(NormArgs p) {
   __shared__ float part[32];
   pdl_trigger();
@@ -98,74 +89,86 @@ __global__ void __launch_bounds__(CPT == 1 || CPT == 2 ? 1024 : 512) rmsnorm_fp8
   }
   const long long row = (long long)blockIdx.x * p.slots + slot;
   const bool live = row < p.rows;
+  bool on[CPT];
   uint4 h[CPT];
+  const uint16_t* x = p.x + row * p.ldx + t * 8;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const uint32_t c = t + k * TPR;
+    on[k] = live && t + k * TPR < p.chunks;
     h[k] = make_uint4(0, 0, 0, 0);
-    if (live && c < p.chunks) h[k] = *reinterpret_cast<const uint4*>(p.x + row * p.ldx + c * 8);
+    if (on[k]) h[k] = *reinterpret_cast<const uint4*>(x + k * TPR * 8);
   }
+  float2 s2 = make_float2(0.0f, 0.0f);
   if (p.residual != nullptr) {
     uint4 r[CPT];
+    const uint16_t* res = p.residual + row * p.ldr + t * 8;
+    uint16_t* out = p.residual_out + row * p.cols + t * 8;
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-      const uint32_t c = t + k * TPR;
       r[k] = make_uint4(0, 0, 0, 0);
-      if (live && c < p.chunks) r[k] = *reinterpret_cast<const uint4*>(p.residual + row * p.ldr + c * 8);
+      if (on[k]) r[k] = *reinterpret_cast<const uint4*>(res + k * TPR * 8);
     }
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
-      const uint32_t c = t + k * TPR;
-      float a[8], b[8];
-      fp4dev::unpack8(h[k], a);
-      fp4dev::unpack8(r[k], b);
+      float2 a[4], b[4];
+      unpack2(h[k], a);
+      unpack2(r[k], b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = __fadd_rn(a[i], b[i]);
-      h[k] = pack8(a);
-      if (live && c < p.chunks) *reinterpret_cast<uint4*>(p.residual_out + row * p.cols + c * 8) = h[k];
+      for (int i = 0; i < 4; ++i) a[i] = fp4dev::add2(a[i], b[i]);
+      h[k] = make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y), pack_bf16(a[2].x, a[2].y),
+                        pack_bf16(a[3].x, a[3].y));
+      if (on[k]) *reinterpret_cast<uint4*>(out + k * TPR * 8) = h[k];
     }
   }
-  float ss = 0.0f;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    float a[8];
-    fp4dev::unpack8(h[k], a);
+    float2 a[4];
+    unpack2(h[k], a);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __fmaf_rn(a[i], a[i], ss);
+    for (int i = 0; i < 4; ++i) s2 = __ffma2_rn(a[i], a[i], s2);
   }
-  ss = row_sum<WARP>(ss, part, slot * (TPR / 32), TPR / 32);
+  const float ss = row_sum<WARP>(__fadd_rn(s2.x, s2.y), part, slot * (TPR / 32), TPR / 32);
   const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, p.fcols), p.eps));
   if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+  const float2 r2 = make_float2(rstd, rstd);
+  float2 y[CPT][4];
+  uint32_t m[CPT];
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
-    const uint32_t c = t + k * TPR;
-    const bool on = live && c < p.chunks;
-    float y[8];
-    fp4dev::unpack8(h[k], y);
-    uint32_t m = 0;
-    if (on) {
+    unpack2(h[k], y[k]);
+    float am = 0.0f;
+    if (on[k]) {
       float w[8];
-      load_weight8(p.weight, p.weight_f32, c, w);
+      load_weight8(p.weight, p.weight_f32, t + k * TPR, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = __fmul_rn(__fmul_rn(y[i], rstd), w[i]);
-        m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+      for (int i = 0; i < 4; ++i) {
+        y[k][i] = __fmul2_rn(__fmul2_rn(y[k][i], r2), make_float2(w[2 * i], w[2 * i + 1]));
+        am = max_abs3(am, y[k][i].x, y[k][i].y);
       }
     }
-    m = max_half_warp(m);
-    const uint32_t byte = p.fmt == 0 ? scale_byte<0>(m) : scale_byte<1>(m);
-    const float inv = inv_scale(byte);
-    const uint32_t g = c >> 4;
-    if (on) {
-      *reinterpret_cast<uint2*>(p.codes + row * p.ldc + c * 8) = p.fmt == 0 ? codes8<0>(y, inv) : codes8<1>(y, inv);
-      if (p.norm_out != nullptr) *reinterpret_cast<uint4*>(p.norm_out + row * p.cols + c * 8) = pack8(y);
+    m[k] = __float_as_uint(am) & 0x7FFFFFFFu;
+  }
+  float inv[CPT];
+  int own;
+  bool stores;
+  const uint32_t byte = block_scales<FMT>(m, inv, own, stores);
+  uint8_t* codes = p.codes + row * p.ldc + t * 8;
+#pragma unroll
+  for (int k = 0; k < CPT; ++k) {
+    if (on[k]) {
+      *reinterpret_cast<uint2*>(codes + k * TPR * 8) = codes8<FMT>(y[k], inv[k]);
+      if (p.norm_out != nullptr)
+        *reinterpret_cast<uint4*>(p.norm_out + row * p.cols + (t + k * TPR) * 8) =
+            make_uint4(pack_bf16(y[k][0].x, y[k][0].y), pack_bf16(y[k][1].x, y[k][1].y),
+                       pack_bf16(y[k][2].x, y[k][2].y), pack_bf16(y[k][3].x, y[k][3].y));
     }
-    if (live && g < p.groups) {
-      const uint32_t j = c & 15u;
-      if (j == 0) p.scales[sf_offset(p.sf_mma, row, g, p.groups)] = (uint8_t)byte;
-      else if (p.sf_mma && g + 1 == p.groups && j <= ((4u - (p.groups & 3u)) & 3u))
-        p.scales[sf_offset(1, row, g + j, p.groups)] = 0;            // groups that pad the layout to 4
-    }
+  }
+  const uint32_t g = (t + own * TPR) >> 4;
+  if (stores && live && own < CPT && g < p.groups) {
+    uint8_t* out = p.scales + sf_offset(p.sf_mma, row, g, p.groups);
+    *out = (uint8_t)byte;
+    if (p.sf_mma && g + 1 == p.groups)                              // groups that pad the layout to 4
+      for (uint32_t k = 1; (g + k) & 3u; ++k) out[k] = 0;
   }
 }
 
@@ -483,8 +486,10 @@ RowShape row_shape(int64_t chunks) {
 }
 
 template <int CPT, bool WARP>
-cudaError_t run_norm(const NormArgs& p, uint32_t grid, cudaStream_t st) {
-  return launch_kernel(rmsnorm_fp8_kernel<CPT, WARP>, dim3(grid), dim3(p.tpr * p.slots), 0, st, false, 1u, p);
+cudaError_t run_norm(const NormArgs& p, int fmt, uint32_t grid, cudaStream_t st) {
+  const dim3 block(p.tpr * p.slots);
+  return fmt == FP8_E4M3_CODES ? launch_kernel(rmsnorm_fp8_kernel<0, CPT, WARP>, dim3(grid), block, 0, st, false, 1u, p)
+                               : launch_kernel(rmsnorm_fp8_kernel<1, CPT, WARP>, dim3(grid), block, 0, st, false, 1u, p);
 }
 
 template <int CPT>
@@ -531,7 +536,6 @@ cudaError_t launch_rmsnorm_fp8(const RmsNormParams& q, int num_sms, cudaStream_t
   p.groups = (uint32_t)fp8_groups(q.cols);
   p.main_ctas = 0;
   p.weight_f32 = q.weight_f32;
-  p.fmt = q.fmt;
   p.sf_mma = q.sf_mma;
   // With fewer rows than SMs nothing hides a row's latency but its own width: as many threads as it has chunks.
   RowShape shape = row_shape(p.chunks);
@@ -545,16 +549,16 @@ cudaError_t launch_rmsnorm_fp8(const RmsNormParams& q, int num_sms, cudaStream_t
   const uint32_t grid = p.main_ctas + (p.sf_mma && q.rows % 128 != 0 ? 1u : 0u);
   if (shape.tpr == 32) {
     switch (shape.cpt) {
-      case 1: return run_norm<1, true>(p, grid, st);
-      case 2: return run_norm<2, true>(p, grid, st);
-      case 3: return run_norm<3, true>(p, grid, st);
-      default: return run_norm<4, true>(p, grid, st);
+      case 1: return run_norm<1, true>(p, q.fmt, grid, st);
+      case 2: return run_norm<2, true>(p, q.fmt, grid, st);
+      case 3: return run_norm<3, true>(p, q.fmt, grid, st);
+      default: return run_norm<4, true>(p, q.fmt, grid, st);
     }
   }
   switch (shape.cpt) {
-    case 1: return run_norm<1, false>(p, grid, st);
-    case 2: return run_norm<2, false>(p, grid, st);
-    default: return run_norm<4, false>(p, grid, st);
+    case 1: return run_norm<1, false>(p, q.fmt, grid, st);
+    case 2: return run_norm<2, false>(p, q.fmt, grid, st);
+    default: return run_norm<4, false>(p, q.fmt, grid, st);
   }
 }
 
