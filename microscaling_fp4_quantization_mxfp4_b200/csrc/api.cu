@@ -20,7 +20,6 @@ using namespace fp4lib;
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxTileRows = 65532;      // row tiles of 128: the grid's second dimension
 
 struct DeviceState {
   bool ready = false;
@@ -211,6 +210,10 @@ fp4_status check_codes(const void* codes, int64_t len, int64_t ldc) {
 fp4_status check_scales(const void* scales, int sf_layout) {
   if (scales == nullptr || !sf_layout_ok(sf_layout)) return FP4_ERR_ARG;
   return sf_layout == FP4_SF_MMA && (reinterpret_cast<uintptr_t>(scales) & 3u) != 0 ? FP4_ERR_ALIGN : FP4_OK;
+}
+// 128 x 128 tiles, the padding's among them, counted in 32 bits.
+bool tiles_fit(int64_t rows, int64_t cols) {
+  return round_up(fp8_groups(rows), 4) * round_up(fp8_groups(cols), 4) < (int64_t)1 << 31;
 }
 fp4_status check_norm_shape(int64_t rows, int64_t cols, const void* weight, int weight_dtype) {
   if (rows <= 0 || cols <= 0 || weight == nullptr) return FP4_ERR_ARG;
@@ -496,9 +499,7 @@ fp4_status fp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t l
   if ((s = check_codes(codes, axis == 1 ? cols : rows, ldc)) != FP4_OK) return s;
   if ((s = check_scales(scales, sf_layout)) != FP4_OK) return s;
   if (axis == 1 && rows * fp8_groups(cols) >= (int64_t)1 << 31) return FP4_ERR_SHAPE;      // 32-bit block index
-  if (axis == 0 && fp8_groups(rows) > kMaxTileRows) return FP4_ERR_SHAPE;
-  int sms = 0;
-  if ((s = device_sms(&sms)) != FP4_OK) return s;
+  if (axis == 0 && !tiles_fit(rows, cols)) return FP4_ERR_SHAPE;
   Fp8QuantizeParams p = {};
   p.x = x;
   p.rows = rows;
@@ -511,12 +512,14 @@ fp4_status fp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t l
     p.codes = codes;
     p.ldc = ldc;
     p.scales = scales;
-    return from_cuda(launch_fp8_quantize_rows(p, sms, st));
+    return from_cuda(launch_fp8_quantize_rows(p, st));
   }
+  int sms = 0;
+  if ((s = device_sms(&sms)) != FP4_OK) return s;
   p.codes_t = codes;
   p.ldc_t = ldc;
   p.scales_t = scales;
-  return from_cuda(launch_fp8_quantize_cols(p, st));
+  return from_cuda(launch_fp8_quantize_cols(p, sms, st));
 }
 
 fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_t ld, int fmt, uint8_t* codes,
@@ -531,7 +534,9 @@ fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_
     if ((s = check_codes(codes_t, rows, ldc_t)) != FP4_OK) return s;
     if ((s = check_scales(scales_t, sf_layout)) != FP4_OK) return s;
   }
-  if (fp8_groups(rows) > kMaxTileRows) return FP4_ERR_SHAPE;
+  if (!tiles_fit(rows, cols)) return FP4_ERR_SHAPE;
+  int sms = 0;
+  if ((s = device_sms(&sms)) != FP4_OK) return s;
   Fp8QuantizeParams p = {};
   p.x = x;
   p.rows = rows;
@@ -545,7 +550,7 @@ fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_
   p.ldc_t = ldc_t;
   p.scales_t = scales_t;
   p.sf_mma = sf_layout == FP4_SF_MMA;
-  return from_cuda(launch_fp8_quantize_tiles(p, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_fp8_quantize_tiles(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 fp4_status fp4_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,

@@ -96,13 +96,17 @@ __global__ void __launch_bounds__(kRowThreads) fp8_quantize_rows_kernel(RowArgs 
 }
 
 // ------------------------------------------- blocks along columns, and tiles --
-// A CTA takes 128 x 128 elements: eight 16-byte loads a thread, kept in registers and copied to shared
-// memory.  TILE = false: every column of the tile is one block of the transpose.  TILE = true: one
-// scale for the tile; the row codes are made from the registers, the transpose's from shared memory.
-// In the column phase a lane reads two adjacent columns (32 lanes: 64 columns, no bank conflicts) of
-// 32 rows, so that its codes of a column are 32 contiguous bytes of the transpose.
+// 128 x 128 elements at a time: persistent CTAs walk the tiles, the next one's 32 KB on their way to the other
+// of two shared-memory buffers (cp.async, zeros past the matrix) while this one is worked on.
+// TILE = false: every column of the tile is one block of the transpose.  TILE = true: one scale for the
+// tile, its codes written along the rows and, unless codes_t is null, along the columns.  In the column
+// phase a lane reads two adjacent columns (32 lanes: 64 columns, no bank conflicts) of 32 rows; the codes pass
+// through the tile's own buffer, so that eight lanes store a whole 128-byte row of the transpose (32 bytes a
+// lane, straight from registers, touched 32 lines an instruction).  Bound by HBM (3 or 4 bytes an element).
 constexpr int kTileThreads = 256;
 constexpr int kTileLoads = 8;           // 16-byte chunks a thread
+constexpr int kTileBytes = 128 * 128 * 2;
+constexpr int kTileBlocks = 3;          // CTAs an SM
 
 struct TileArgs {
   const uint16_t* x;
@@ -112,30 +116,33 @@ struct TileArgs {
   uint8_t* codes_t;
   uint8_t* scales_t;
   long long groups, groups_t;
+  uint32_t tiles, tiles_x;      // tiles to visit, of which tiles_x side by side
   int sf_mma;
 };
 
-// 32 codes of one column into the transpose's row `dst` (32 elements, `n` of them inside).
-__device__ __forceinline__ void store_codes32(uint8_t* dst, const uint32_t (&w)[8], int n) {
-  if (n >= 32) {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
+__device__ __forceinline__ void tile_fetch(const TileArgs& p, uint32_t index, uint32_t* buf) {
+  if (index < p.tiles) {
+    const long long rt = index / p.tiles_x, ct = index - rt * p.tiles_x;
+    const int r = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
+    const long long row = rt * 128 + r, col = ct * 128 + c;
+    const uint16_t* src = p.x + row * p.ld + col;
+    const uint32_t dst = fp4dev::smem_addr(buf) + threadIdx.x * 16;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) dst[i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
+    for (int i = 0; i < kTileLoads; ++i) {
+      const bool in = row + 16 * i < p.rows && col < p.cols;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * kTileThreads * 16),
+                   "l"(in ? src + 16 * i * p.ld : p.x), "r"(in ? 16 : 0)
+                   : "memory");
+    }
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 template <int FMT, bool TILE>
-__global__ void __launch_bounds__(kTileThreads) fp8_quantize_tile_kernel(TileArgs p) {
-  pdl_trigger();
-  __shared__ uint32_t tile[128 * 64];             // bf16 pairs, row-major
-  __shared__ uint32_t red[4 * 64];                // column maxima of the four 32-row groups / warps' maxima
+__device__ __forceinline__ void tile_codes(const TileArgs& p, long long rt, long long ct, uint32_t* tile,
+                                           uint32_t* red) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const long long rt = blockIdx.y, ct = blockIdx.x;              // row and column tile
   const long long r0 = rt * 128, c0 = ct * 128;
-  pdl_wait();
   if (r0 >= p.rows || c0 >= p.cols) {
     // a tile of the layout's padding: its scales are zero
     if (t < 128) {
@@ -144,49 +151,38 @@ __global__ void __launch_bounds__(kTileThreads) fp8_quantize_tile_kernel(TileArg
     }
     return;
   }
-  uint4 v[kTileLoads];
-#pragma unroll
-  for (int i = 0; i < kTileLoads; ++i) {
-    const int r = (t >> 4) + 16 * i, c = (t & 15) * 8;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (r0 + r < p.rows && c0 + c < p.cols)
-      v[i] = *reinterpret_cast<const uint4*>(p.x + (r0 + r) * p.ld + c0 + c);
-  }
-  const bool want_t = !TILE || p.codes_t != nullptr;
-  if (want_t) {
-#pragma unroll
-    for (int i = 0; i < kTileLoads; ++i)
-      *reinterpret_cast<uint4*>(&tile[((t >> 4) + 16 * i) * 64 + (t & 15) * 4]) = v[i];
-  }
   uint32_t byte = 0;
   if (TILE) {
+    uint4 v[kTileLoads];
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kTileLoads; ++i) m = __vmaxu2(m, max_abs8(v[i]));
+    for (int i = 0; i < kTileLoads; ++i) {
+      v[i] = reinterpret_cast<const uint4*>(tile)[t + i * kTileThreads];
+      m = __vmaxu2(m, max_abs8(v[i]));
+    }
     m = __reduce_max_sync(0xFFFFFFFFu, pair_bits(m));
     if (lane == 0) red[warp] = m;
-  }
-  __syncthreads();
-  if (TILE) {
-    uint32_t m = 0;
+    __syncthreads();
+    m = 0;
 #pragma unroll
     for (int w = 0; w < kTileThreads / 32; ++w) m = max(m, red[w]);
     byte = scale_byte<FMT>(m);
     const float inv = inv_scale(byte);
+    const int r = t >> 4, c = (t & 15) * 8;
+    uint8_t* dst = p.codes + (r0 + r) * p.ldc + c0 + c;
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) {
-      const int r = (t >> 4) + 16 * i, c = (t & 15) * 8;
-      if (r0 + r < p.rows && c0 + c < p.cols) {
+      if (r0 + r + 16 * i < p.rows && c0 + c < p.cols) {
         float2 e[4];
         unpack2(v[i], e);
-        *reinterpret_cast<uint2*>(p.codes + (r0 + r) * p.ldc + c0 + c) = codes8<FMT>(e, inv);
+        *reinterpret_cast<uint2*>(dst + 16 * i * p.ldc) = codes8<FMT>(e, inv);
       }
     }
     if (t < 128) {
       if (r0 + t < p.rows) p.scales[sf_offset(p.sf_mma, r0 + t, ct, p.groups)] = (uint8_t)byte;
       else if (p.sf_mma) p.scales[sf_offset(1, r0 + t, ct, p.groups)] = 0;
     }
-    if (!want_t) return;
+    if (p.codes_t == nullptr) return;
   }
   // columns: lane -> pair of columns in half `warp & 1`, rows 32 * (warp >> 1) .. + 31
   const int pr = (warp & 1) * 32 + lane, rg = warp >> 1;
@@ -204,32 +200,70 @@ __global__ void __launch_bounds__(kTileThreads) fp8_quantize_tile_kernel(TileArg
     blo = scale_byte<FMT>(m << 16);
     bhi = scale_byte<FMT>(m & 0xFFFF0000u);
   }
-  const float ilo = inv_scale(blo), ihi = inv_scale(bhi);
-  const long long c = c0 + 2 * pr;                        // even, and cols is a multiple of 8: both inside or both out
-  if (c < p.cols) {
-    uint32_t lo[8], hi[8];
+  const float2 inv = make_float2(inv_scale(blo), inv_scale(bhi));
+  uint32_t lo[8], hi[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      lo[k] = cvt4<FMT>(__fmul_rn(fp4dev::bf16_lo(w[4 * k]), ilo), __fmul_rn(fp4dev::bf16_lo(w[4 * k + 1]), ilo),
-                        __fmul_rn(fp4dev::bf16_lo(w[4 * k + 2]), ilo), __fmul_rn(fp4dev::bf16_lo(w[4 * k + 3]), ilo));
-      hi[k] = cvt4<FMT>(__fmul_rn(fp4dev::bf16_hi(w[4 * k]), ihi), __fmul_rn(fp4dev::bf16_hi(w[4 * k + 1]), ihi),
-                        __fmul_rn(fp4dev::bf16_hi(w[4 * k + 2]), ihi), __fmul_rn(fp4dev::bf16_hi(w[4 * k + 3]), ihi));
-    }
-    const long long left = p.rows - (r0 + rg * 32);
-    if (left > 0) {
-      uint8_t* dst = p.codes_t + c * p.ldc_t + r0 + rg * 32;
-      const int n = left < 32 ? (int)left : 32;
-      store_codes32(dst, lo, n);
-      store_codes32(dst + p.ldc_t, hi, n);
-    }
-    if (rg == 0) {
-      p.scales_t[sf_offset(p.sf_mma, c, rt, p.groups_t)] = (uint8_t)blo;
-      p.scales_t[sf_offset(p.sf_mma, c + 1, rt, p.groups_t)] = (uint8_t)bhi;
-    }
-  } else if (p.sf_mma && rg == 0) {
-    p.scales_t[sf_offset(1, c, rt, p.groups_t)] = 0;
-    p.scales_t[sf_offset(1, c + 1, rt, p.groups_t)] = 0;
+  for (int k = 0; k < 8; ++k) {
+    float2 e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      e[i] = __fmul2_rn(make_float2(fp4dev::bf16_lo(w[4 * k + i]), fp4dev::bf16_hi(w[4 * k + i])), inv);
+    lo[k] = cvt4<FMT>(e[0].x, e[1].x, e[2].x, e[3].x);
+    hi[k] = cvt4<FMT>(e[0].y, e[1].y, e[2].y, e[3].y);
   }
+  const long long c = c0 + 2 * pr;                        // even, and cols is a multiple of 8: both inside or both out
+  if (rg == 0 && (c < p.cols || p.sf_mma)) {
+    const bool in = c < p.cols;                           // else a row that pads the layout
+    p.scales_t[sf_offset(p.sf_mma, c, rt, p.groups_t)] = in ? (uint8_t)blo : 0;
+    p.scales_t[sf_offset(p.sf_mma, c + 1, rt, p.groups_t)] = in ? (uint8_t)bhi : 0;
+  }
+  if (TILE) __syncthreads();                              // the tile has been read (the maxima's barrier, without TILE)
+  // 128 rows of 128 codes, 16-byte piece j of row r at j ^ (r / 2 mod 8): the two rows of a lane, and then a
+  // row's eight pieces, fall on distinct banks
+  uint4* out = reinterpret_cast<uint4*>(tile);
+  const int sw = pr & 7;
+  out[2 * pr * 8 + ((2 * rg) ^ sw)] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  out[2 * pr * 8 + ((2 * rg + 1) ^ sw)] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+  out[(2 * pr + 1) * 8 + ((2 * rg) ^ sw)] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  out[(2 * pr + 1) * 8 + ((2 * rg + 1) ^ sw)] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+  __syncthreads();
+  const int piece = t & 7;
+  const long long left = p.rows - (r0 + piece * 16);      // elements of the transpose's rows from this piece on
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (t >> 3) + 32 * i;
+    if (c0 + r >= p.cols || left <= 0) break;
+    const uint4 v = out[r * 8 + (piece ^ ((r >> 1) & 7))];
+    uint8_t* dst = p.codes_t + (c0 + r) * p.ldc_t + r0 + piece * 16;
+    if (left >= 16) {
+      *reinterpret_cast<uint4*>(dst) = v;
+    } else {
+      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int b = 0; b < 15; ++b)
+        if (b < left) dst[b] = (uint8_t)(q[b / 4] >> (8 * (b & 3)));
+    }
+  }
+}
+
+template <int FMT, bool TILE>
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks) fp8_quantize_tile_kernel(TileArgs p) {
+  extern __shared__ __align__(128) uint8_t buffers[];       // two tiles of bf16 pairs, row-major
+  __shared__ uint32_t red[4 * 64];                          // column maxima of the four 32-row groups / warps' maxima
+  uint32_t* buf = reinterpret_cast<uint32_t*>(buffers);
+  pdl_trigger();
+  pdl_wait();
+  tile_fetch(p, blockIdx.x, buf);
+  int at = 0;
+  for (uint32_t index = blockIdx.x; index < p.tiles; index += gridDim.x, at ^= 1) {
+    tile_fetch(p, index + gridDim.x, buf + (at ^ 1) * (kTileBytes / 4));
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const uint32_t rt = index / p.tiles_x;
+    tile_codes<FMT, TILE>(p, rt, index - rt * p.tiles_x, buf + at * (kTileBytes / 4), red);
+    __syncthreads();                                        // every thread has read the buffer that is filled next
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------- dequantize --
@@ -298,8 +332,7 @@ __global__ void __launch_bounds__(256) fp8_dequantize_kernel(DeqArgs p) {
 
 }  // namespace
 
-cudaError_t launch_fp8_quantize_rows(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+cudaError_t launch_fp8_quantize_rows(const Fp8QuantizeParams& q, cudaStream_t st) {
   RowArgs p;
   p.x = static_cast<const uint16_t*>(q.x);
   p.rows = q.rows;
@@ -319,8 +352,18 @@ cudaError_t launch_fp8_quantize_rows(const Fp8QuantizeParams& q, int num_sms, cu
              : launch_kernel(fp8_quantize_rows_kernel<1>, dim3(grid), dim3(kRowThreads), 0, st, false, 1u, p);
 }
 
+template <int FMT, bool TILE>
+static cudaError_t run_tiles(const TileArgs& p, int num_sms, cudaStream_t st) {
+  auto kernel = fp8_quantize_tile_kernel<FMT, TILE>;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kTileBytes);
+  if (attr != cudaSuccess) return attr;
+  const uint32_t grid = std::min<uint32_t>(p.tiles, (uint32_t)(num_sms * kTileBlocks));
+  return launch_kernel(kernel, dim3(grid), dim3(kTileThreads), 2 * kTileBytes, st, false, 1u, p);
+}
+
 template <bool TILE>
-static cudaError_t launch_tiles(const Fp8QuantizeParams& q, cudaStream_t st) {
+static cudaError_t launch_tiles(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
   TileArgs p;
   p.x = static_cast<const uint16_t*>(q.x);
   p.rows = q.rows;
@@ -340,14 +383,17 @@ static cudaError_t launch_tiles(const Fp8QuantizeParams& q, cudaStream_t st) {
     if (TILE) gx = (gx + 3) / 4 * 4;
     if (q.scales_t != nullptr) gy = (gy + 3) / 4 * 4;
   }
-  const dim3 grid((unsigned)gx, (unsigned)gy);
-  return q.fmt == FP8_E4M3_CODES
-             ? launch_kernel(fp8_quantize_tile_kernel<0, TILE>, grid, dim3(kTileThreads), 0, st, false, 1u, p)
-             : launch_kernel(fp8_quantize_tile_kernel<1, TILE>, grid, dim3(kTileThreads), 0, st, false, 1u, p);
+  p.tiles_x = (uint32_t)gx;
+  p.tiles = (uint32_t)(gx * gy);
+  return q.fmt == FP8_E4M3_CODES ? run_tiles<0, TILE>(p, num_sms, st) : run_tiles<1, TILE>(p, num_sms, st);
 }
 
-cudaError_t launch_fp8_quantize_cols(const Fp8QuantizeParams& q, cudaStream_t st) { return launch_tiles<false>(q, st); }
-cudaError_t launch_fp8_quantize_tiles(const Fp8QuantizeParams& q, cudaStream_t st) { return launch_tiles<true>(q, st); }
+cudaError_t launch_fp8_quantize_cols(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
+  return launch_tiles<false>(q, num_sms, st);
+}
+cudaError_t launch_fp8_quantize_tiles(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
+  return launch_tiles<true>(q, num_sms, st);
+}
 
 cudaError_t launch_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,
                                   int fmt, int sf_mma, void* out, int out_bf16, cudaStream_t st) {

@@ -39,9 +39,9 @@ def test_quantize_refusals(lib):
             (4, 2, ARG), (4, -1, ARG), (5, 2, ARG), (6, None, ARG), (6, FAKE + 8, ALIGN), (7, 48, ARG), (7, 72, ALIGN),
             (8, None, ARG), (8, FAKE + 2, ALIGN), (9, 2, ARG), (1, 1 << 31, SHAPE)]):
         assert lib.fp4_fp8_quantize(*args) == status, args
-    # axis 0: the row stride of the codes is at least the number of rows; the grid's limit on row tiles
+    # axis 0: the row stride of the codes is at least the number of rows; tiles are counted in 32 bits
     assert lib.fp4_fp8_quantize(FAKE, 100, 64, 64, 0, 0, FAKE, 96, FAKE, 1, None) == ARG
-    assert lib.fp4_fp8_quantize(FAKE, 1 << 24, 64, 64, 0, 0, FAKE, 1 << 24, FAKE, 1, None) == SHAPE
+    assert lib.fp4_fp8_quantize(FAKE, (1 << 31) - 16, 16384, 16384, 0, 0, FAKE, 1 << 31, FAKE, 1, None) == SHAPE
 
 
 def test_quantize_2d_refusals(lib):
