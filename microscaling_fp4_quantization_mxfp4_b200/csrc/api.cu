@@ -514,12 +514,10 @@ fp4_status fp4_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t l
     p.scales = scales;
     return from_cuda(launch_fp8_quantize_rows(p, st));
   }
-  int sms = 0;
-  if ((s = device_sms(&sms)) != FP4_OK) return s;
   p.codes_t = codes;
   p.ldc_t = ldc;
   p.scales_t = scales;
-  return from_cuda(launch_fp8_quantize_cols(p, sms, st));
+  return from_cuda(launch_fp8_quantize_cols(p, st));
 }
 
 fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_t ld, int fmt, uint8_t* codes,
@@ -535,8 +533,6 @@ fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_
     if ((s = check_scales(scales_t, sf_layout)) != FP4_OK) return s;
   }
   if (!tiles_fit(rows, cols)) return FP4_ERR_SHAPE;
-  int sms = 0;
-  if ((s = device_sms(&sms)) != FP4_OK) return s;
   Fp8QuantizeParams p = {};
   p.x = x;
   p.rows = rows;
@@ -550,7 +546,7 @@ fp4_status fp4_fp8_quantize_2d(const void* x, int64_t rows, int64_t cols, int64_
   p.ldc_t = ldc_t;
   p.scales_t = scales_t;
   p.sf_mma = sf_layout == FP4_SF_MMA;
-  return from_cuda(launch_fp8_quantize_tiles(p, sms, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_fp8_quantize_tiles(p, static_cast<cudaStream_t>(stream)));
 }
 
 fp4_status fp4_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,

@@ -96,17 +96,17 @@ __global__ void __launch_bounds__(kRowThreads) fp8_quantize_rows_kernel(RowArgs 
 }
 
 // ------------------------------------------- blocks along columns, and tiles --
-// 128 x 128 elements at a time: persistent CTAs walk the tiles, the next one's 32 KB on their way to the other
-// of two shared-memory buffers (cp.async, zeros past the matrix) while this one is worked on.
-// TILE = false: every column of the tile is one block of the transpose.  TILE = true: one scale for the
-// tile, its codes written along the rows and, unless codes_t is null, along the columns.  In the column
-// phase a lane reads two adjacent columns (32 lanes: 64 columns, no bank conflicts) of 32 rows; the codes pass
-// through the tile's own buffer, so that eight lanes store a whole 128-byte row of the transpose (32 bytes a
-// lane, straight from registers, touched 32 lines an instruction).  Bound by HBM (3 or 4 bytes an element).
+// 128 x 128 elements a CTA, copied to shared memory by cp.async (zeros past the matrix).  TILE = false: every
+// column of the tile is one block of the transpose.  TILE = true: one scale for the tile, its codes written
+// along the rows and, unless codes_t is null, along the columns.  In the column phase a lane reads two adjacent
+// columns (32 lanes: 64 columns, no bank conflicts) of 32 rows; the codes pass through the tile's own buffer, so
+// that eight lanes store a whole 128-byte row of the transpose (32 bytes a lane, straight from registers,
+// touched 32 lines an instruction: 46.6 us for 16301 x 4096).  Bound by HBM (3 or 4 bytes an element).  What is
+// in flight is the other CTAs' tiles: five an SM (48 registers) took 34.2 us, six, which spill, 35.6, three
+// persistent ones with a second buffer for the next tile 37.1.
 constexpr int kTileThreads = 256;
 constexpr int kTileLoads = 8;           // 16-byte chunks a thread
-constexpr int kTileBytes = 128 * 128 * 2;
-constexpr int kTileBlocks = 3;          // CTAs an SM
+constexpr int kTileBlocks = 5;          // CTAs an SM
 
 struct TileArgs {
   const uint16_t* x;
@@ -116,33 +116,19 @@ struct TileArgs {
   uint8_t* codes_t;
   uint8_t* scales_t;
   long long groups, groups_t;
-  uint32_t tiles, tiles_x;      // tiles to visit, of which tiles_x side by side
+  uint32_t tiles_x;             // tiles side by side
   int sf_mma;
 };
 
-__device__ __forceinline__ void tile_fetch(const TileArgs& p, uint32_t index, uint32_t* buf) {
-  if (index < p.tiles) {
-    const long long rt = index / p.tiles_x, ct = index - rt * p.tiles_x;
-    const int r = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
-    const long long row = rt * 128 + r, col = ct * 128 + c;
-    const uint16_t* src = p.x + row * p.ld + col;
-    const uint32_t dst = fp4dev::smem_addr(buf) + threadIdx.x * 16;
-#pragma unroll
-    for (int i = 0; i < kTileLoads; ++i) {
-      const bool in = row + 16 * i < p.rows && col < p.cols;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * kTileThreads * 16),
-                   "l"(in ? src + 16 * i * p.ld : p.x), "r"(in ? 16 : 0)
-                   : "memory");
-    }
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
 template <int FMT, bool TILE>
-__device__ __forceinline__ void tile_codes(const TileArgs& p, long long rt, long long ct, uint32_t* tile,
-                                           uint32_t* red) {
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks) fp8_quantize_tile_kernel(TileArgs p) {
+  __shared__ __align__(128) uint32_t tile[128 * 64];        // bf16 pairs, row-major
+  __shared__ uint32_t red[4 * 64];                          // column maxima of the four 32-row groups / warps' maxima
+  pdl_trigger();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const long long rt = blockIdx.x / p.tiles_x, ct = blockIdx.x - rt * p.tiles_x;
   const long long r0 = rt * 128, c0 = ct * 128;
+  pdl_wait();
   if (r0 >= p.rows || c0 >= p.cols) {
     // a tile of the layout's padding: its scales are zero
     if (t < 128) {
@@ -151,6 +137,20 @@ __device__ __forceinline__ void tile_codes(const TileArgs& p, long long rt, long
     }
     return;
   }
+  {
+    const long long row = r0 + (t >> 4), col = c0 + (t & 15) * 8;
+    const uint16_t* src = p.x + row * p.ld + col;
+    const uint32_t dst = fp4dev::smem_addr(tile) + t * 16;
+#pragma unroll
+    for (int i = 0; i < kTileLoads; ++i) {
+      const bool in = row + 16 * i < p.rows && col < p.cols;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * kTileThreads * 16),
+                   "l"(in ? src + 16 * i * p.ld : p.x), "r"(in ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+  }
+  __syncthreads();
   uint32_t byte = 0;
   if (TILE) {
     uint4 v[kTileLoads];
@@ -246,26 +246,6 @@ __device__ __forceinline__ void tile_codes(const TileArgs& p, long long rt, long
   }
 }
 
-template <int FMT, bool TILE>
-__global__ void __launch_bounds__(kTileThreads, kTileBlocks) fp8_quantize_tile_kernel(TileArgs p) {
-  extern __shared__ __align__(128) uint8_t buffers[];       // two tiles of bf16 pairs, row-major
-  __shared__ uint32_t red[4 * 64];                          // column maxima of the four 32-row groups / warps' maxima
-  uint32_t* buf = reinterpret_cast<uint32_t*>(buffers);
-  pdl_trigger();
-  pdl_wait();
-  tile_fetch(p, blockIdx.x, buf);
-  int at = 0;
-  for (uint32_t index = blockIdx.x; index < p.tiles; index += gridDim.x, at ^= 1) {
-    tile_fetch(p, index + gridDim.x, buf + (at ^ 1) * (kTileBytes / 4));
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();
-    const uint32_t rt = index / p.tiles_x;
-    tile_codes<FMT, TILE>(p, rt, index - rt * p.tiles_x, buf + at * (kTileBytes / 4), red);
-    __syncthreads();                                        // every thread has read the buffer that is filled next
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
 // ------------------------------------------------------------- dequantize --
 // One thread per 8 codes of a row: value = code * 2^(byte - 127) in fp32 (exact wherever the product
 // is a normal fp32 number), rounded to bf16 on request.
@@ -352,18 +332,8 @@ cudaError_t launch_fp8_quantize_rows(const Fp8QuantizeParams& q, cudaStream_t st
              : launch_kernel(fp8_quantize_rows_kernel<1>, dim3(grid), dim3(kRowThreads), 0, st, false, 1u, p);
 }
 
-template <int FMT, bool TILE>
-static cudaError_t run_tiles(const TileArgs& p, int num_sms, cudaStream_t st) {
-  auto kernel = fp8_quantize_tile_kernel<FMT, TILE>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kTileBytes);
-  if (attr != cudaSuccess) return attr;
-  const uint32_t grid = std::min<uint32_t>(p.tiles, (uint32_t)(num_sms * kTileBlocks));
-  return launch_kernel(kernel, dim3(grid), dim3(kTileThreads), 2 * kTileBytes, st, false, 1u, p);
-}
-
 template <bool TILE>
-static cudaError_t launch_tiles(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
+static cudaError_t launch_tiles(const Fp8QuantizeParams& q, cudaStream_t st) {
   TileArgs p;
   p.x = static_cast<const uint16_t*>(q.x);
   p.rows = q.rows;
@@ -384,16 +354,14 @@ static cudaError_t launch_tiles(const Fp8QuantizeParams& q, int num_sms, cudaStr
     if (q.scales_t != nullptr) gy = (gy + 3) / 4 * 4;
   }
   p.tiles_x = (uint32_t)gx;
-  p.tiles = (uint32_t)(gx * gy);
-  return q.fmt == FP8_E4M3_CODES ? run_tiles<0, TILE>(p, num_sms, st) : run_tiles<1, TILE>(p, num_sms, st);
+  const dim3 grid((unsigned)(gx * gy));
+  return q.fmt == FP8_E4M3_CODES
+             ? launch_kernel(fp8_quantize_tile_kernel<0, TILE>, grid, dim3(kTileThreads), 0, st, false, 1u, p)
+             : launch_kernel(fp8_quantize_tile_kernel<1, TILE>, grid, dim3(kTileThreads), 0, st, false, 1u, p);
 }
 
-cudaError_t launch_fp8_quantize_cols(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
-  return launch_tiles<false>(q, num_sms, st);
-}
-cudaError_t launch_fp8_quantize_tiles(const Fp8QuantizeParams& q, int num_sms, cudaStream_t st) {
-  return launch_tiles<true>(q, num_sms, st);
-}
+cudaError_t launch_fp8_quantize_cols(const Fp8QuantizeParams& q, cudaStream_t st) { return launch_tiles<false>(q, st); }
+cudaError_t launch_fp8_quantize_tiles(const Fp8QuantizeParams& q, cudaStream_t st) { return launch_tiles<true>(q, st); }
 
 cudaError_t launch_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,
                                   int fmt, int sf_mma, void* out, int out_bf16, cudaStream_t st) {

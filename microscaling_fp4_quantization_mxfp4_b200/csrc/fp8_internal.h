@@ -27,9 +27,9 @@ struct Fp8QuantizeParams {
 // 1 x 128 blocks along the rows (codes, scales).
 cudaError_t launch_fp8_quantize_rows(const Fp8QuantizeParams& p, cudaStream_t st);
 // 1 x 128 blocks of the transpose, i.e. along the columns (codes_t, scales_t).
-cudaError_t launch_fp8_quantize_cols(const Fp8QuantizeParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_fp8_quantize_cols(const Fp8QuantizeParams& p, cudaStream_t st);
 // 128 x 128 tiles (codes, scales and, unless null, codes_t, scales_t).
-cudaError_t launch_fp8_quantize_tiles(const Fp8QuantizeParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_fp8_quantize_tiles(const Fp8QuantizeParams& p, cudaStream_t st);
 cudaError_t launch_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t rows, int64_t cols,
                                   int fmt, int sf_mma, void* out, int out_bf16, cudaStream_t st);
 
