@@ -8,7 +8,6 @@ every call raises if libfp4.so is missing or a tensor is not on a GPU.
 """
 from __future__ import annotations
 
-import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -300,83 +299,74 @@ def fp4_nv_tensor_scale(amax: torch.Tensor, *, out=None, stream=None) -> torch.T
 
 
 # ------------------------------------------------------------ 8-bit operators ---
-def _where_it_lives(fn):
-    """Run `fn` with its first tensor's device current and, if given, on `stream`: outputs and workspaces
-    are then allocated for the stream that uses them."""
-    @functools.wraps(fn)
-    def call(x, *args, stream=None, **kwargs):
-        _need_cuda(x, "the first argument")
-        if stream is None and x.get_device() == torch._C._cuda_getDevice():
-            return fn(x, *args, **kwargs)
-        if stream is not None and stream.device != x.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-        with torch.cuda.device(x.device), torch.cuda.stream(stream):
-            return fn(x, *args, **kwargs)
-    return call
+# A small call's time is the host's: the checks below are a comparison each, messages are made where one fails.
+_bf16, _f32, _u8 = torch.bfloat16, torch.float32, torch.uint8
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(x: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} is on {t.device}, the first argument on {x.device}")
+def _elsewhere(fn, x: torch.Tensor, stream, *args, **kwargs):
+    """`fn` with its first tensor's device current and, if given, on `stream`: outputs and workspaces are then
+    allocated for the stream that uses them."""
+    _need_cuda(x, "the first argument")
+    if stream is not None and stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+    with torch.cuda.device(x.device), torch.cuda.stream(stream):
+        return fn(x, *args, **kwargs)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor with unit column stride (a single row's own stride says nothing)."""
-    return t.stride(0) if t.shape[0] != 1 else t.shape[1]
-
-
-def _bf16_rows(x: torch.Tensor, shape, name: str) -> int:
-    if x.dtype != torch.bfloat16 or x.shape != shape or x.stride(1) != 1:
-        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} with unit column stride")
-    return _row_stride(x)
-
-
-def _contiguous(t: torch.Tensor, shape, dtype, name: str) -> torch.Tensor:
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+def _fits(t: torch.Tensor, dev: int, dtype, shape, name: str) -> torch.Tensor:
+    """A contiguous tensor of this dtype and shape on the device."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
     return t
 
 
-def _pitch(t: torch.Tensor) -> int:
+def _bf16_rows(t: torch.Tensor, dev: int, shape, name: str) -> int:
+    """Row stride of a bf16 matrix of this shape (a single row's own stride says nothing)."""
+    if t.get_device() != dev or t.dtype is not _bf16 or t.shape != shape or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} with unit column stride on cuda:{dev}")
+    return t.stride(0) if shape[0] != 1 else shape[1]
+
+
+def _codes8(t: torch.Tensor, dev: int, name: str, shape=None) -> int:
     """Row stride of 8-bit codes (a single row: its length rounded up to 16)."""
-    return t.stride(0) if t.shape[0] != 1 else (t.shape[1] + 15) // 16 * 16
-
-
-def _codes8(t: torch.Tensor, name: str, shape=None) -> int:
-    if t.dtype not in _BYTE or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1) or \
+    if t.get_device() != dev or t.dtype not in _BYTE or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1) or \
             (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be 8-bit codes" + (f" of shape {tuple(shape)}" if shape is not None else
-                                                          ", 2-D") + " with unit column stride")
-    return _pitch(t)
+        raise ValueError(f"{name} must be a matrix of 8-bit codes" +
+                         (f" of shape {tuple(shape)}" if shape is not None else "") + f" with unit column stride on cuda:{dev}")
+    rows, cols = t.shape
+    return t.stride(0) if rows != 1 else (cols + 15) // 16 * 16
 
 
 def _scales_shape(rows: int, length: int, sf: int):
     g = (length + FP8_BLOCK - 1) // FP8_BLOCK
-    return (rows, g) if sf == SF_ROWMAJOR else ((rows + 127) // 128 * 128 * ((g + 3) // 4 * 4),)
+    return ((rows + 127) // 128 * 128 * ((g + 3) // 4 * 4),) if sf == SF_MMA else (rows, g)
 
 
-def _scales8(t: torch.Tensor, rows: int, length: int, sf: int, name: str) -> None:
+def _scales8(t: torch.Tensor, dev: int, rows: int, length: int, sf: int, name: str) -> int:
+    """Address of checked scale bytes."""
     shape = _scales_shape(rows, length, sf)
-    if t.dtype not in _BYTE or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous scale bytes of shape {tuple(shape)}")
+    if t.get_device() != dev or t.dtype not in _BYTE or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous scale bytes of shape {shape} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _fp8_outputs(x, rows, length, sf, codes, scales, name=""):
-    """Checked or new codes [rows, length] and scales; returns (codes, row stride, scales)."""
+def _fp8_outputs(x, dev, rows, length, sf, codes, scales, name=""):
+    """Checked or new codes [rows, length] and scales: (codes, row stride, scales).  New rows that are not whole
+    16-byte pieces are padded to 128 bytes: the product reads 128-byte pieces of them, and rows 16 bytes off
+    the next line cost it a fifth of its rate."""
     if codes is None:
-        pitch = (length + 15) // 16 * 16
-        codes = torch.empty((rows, pitch), dtype=torch.uint8, device=x.device)
-        if pitch != length:
-            codes = codes[:, :length]
+        if length % 16 == 0:
+            pitch, codes = length, x.new_empty((rows, length), dtype=_u8)
+        else:
+            pitch = (length + 127) // 128 * 128
+            codes = x.new_empty((rows, pitch), dtype=_u8)[:, :length]
     else:
-        _same_device(x, **{"codes" + name: codes})
-        pitch = _codes8(codes, "codes" + name, (rows, length))
+        pitch = _codes8(codes, dev, "codes" + name, (rows, length))
     if scales is None:
-        scales = torch.empty(_scales_shape(rows, length, sf), dtype=torch.uint8, device=x.device)
+        scales = x.new_empty(_scales_shape(rows, length, sf), dtype=_u8)
     else:
-        _same_device(x, **{"scales" + name: scales})
-        _scales8(scales, rows, length, sf, "scales" + name)
+        _scales8(scales, dev, rows, length, sf, "scales" + name)
     return codes, pitch, scales
 
 
@@ -386,146 +376,172 @@ def fp4_fp8_scales_bytes(rows: int, cols: int, axis: int, sf_layout="rowmajor") 
     return _lib.load().fp4_fp8_scales_bytes(rows, cols, axis, _SF[sf_layout])
 
 
-@_where_it_lives
-def fp4_fp8_quantize(x: torch.Tensor, fmt="e4m3", axis: int = 1, sf_layout="rowmajor", *, codes=None,
-                     scales=None) -> Fp8Quantized:
+def fp4_fp8_quantize(x: torch.Tensor, fmt="e4m3", axis: int = 1, sf_layout="rowmajor", *, codes=None, scales=None,
+                     stream=None) -> Fp8Quantized:
     """bf16 [rows, cols] -> E4M3 or E5M2 codes with one power-of-two scale per 128 elements along `axis` (0: of
-    the transpose); see fp4_fp8_quantize in include/fp4.h.  `stream=` runs it on that stream."""
+    the transpose); see fp4_fp8_quantize in include/fp4.h."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _device():
+        return _elsewhere(fp4_fp8_quantize, x, stream, fmt, axis, sf_layout, codes=codes, scales=scales)
     _bf16_matrix(x)
     f, sf = _FMT8[fmt], _SF[sf_layout]
     rows, cols = x.shape
     orows, length = (rows, cols) if axis == 1 else (cols, rows)
-    codes, pitch, scales = _fp8_outputs(x, orows, length, sf, codes, scales)
-    _check(_lib.load().fp4_fp8_quantize(x.data_ptr(), rows, cols, _row_stride(x), f, axis, codes.data_ptr(), pitch,
-                                        scales.data_ptr(), sf, _stream(None)), "fp4_fp8_quantize")
+    codes, pitch, scales = _fp8_outputs(x, dev, orows, length, sf, codes, scales)
+    _check(_lib.load().fp4_fp8_quantize(x.data_ptr(), rows, cols, x.stride(0) if rows != 1 else cols, f, axis,
+                                        codes.data_ptr(), pitch, scales.data_ptr(), sf, _raw_stream(dev)),
+           "fp4_fp8_quantize")
     return Fp8Quantized(codes, scales)
 
 
-@_where_it_lives
 def fp4_fp8_quantize_2d(x: torch.Tensor, fmt="e4m3", sf_layout="rowmajor", transposed: bool = True, *, codes=None,
-                        scales=None, codes_t=None, scales_t=None):
+                        scales=None, codes_t=None, scales_t=None, stream=None):
     """One scale per 128 x 128 tile of a bf16 matrix (see fp4_fp8_quantize_2d in include/fp4.h).  Returns
     (W along its rows, W^T along its rows or None) as Fp8Quantized, with the same codes."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _device():
+        return _elsewhere(fp4_fp8_quantize_2d, x, stream, fmt, sf_layout, transposed, codes=codes, scales=scales,
+                          codes_t=codes_t, scales_t=scales_t)
     _bf16_matrix(x)
     f, sf = _FMT8[fmt], _SF[sf_layout]
     rows, cols = x.shape
-    codes, pitch, scales = _fp8_outputs(x, rows, cols, sf, codes, scales)
+    codes, pitch, scales = _fp8_outputs(x, dev, rows, cols, sf, codes, scales)
     pitch_t = 0
     if transposed:
-        codes_t, pitch_t, scales_t = _fp8_outputs(x, cols, rows, sf, codes_t, scales_t, "_t")
+        codes_t, pitch_t, scales_t = _fp8_outputs(x, dev, cols, rows, sf, codes_t, scales_t, "_t")
     else:
         codes_t = scales_t = None
-    _check(_lib.load().fp4_fp8_quantize_2d(x.data_ptr(), rows, cols, _row_stride(x), f, codes.data_ptr(), pitch,
-                                           scales.data_ptr(), _ptr(codes_t), pitch_t, _ptr(scales_t), sf,
-                                           _stream(None)), "fp4_fp8_quantize_2d")
+    _check(_lib.load().fp4_fp8_quantize_2d(x.data_ptr(), rows, cols, x.stride(0) if rows != 1 else cols, f,
+                                           codes.data_ptr(), pitch, scales.data_ptr(), _ptr(codes_t), pitch_t,
+                                           _ptr(scales_t), sf, _raw_stream(dev)), "fp4_fp8_quantize_2d")
     return Fp8Quantized(codes, scales), (Fp8Quantized(codes_t, scales_t) if transposed else None)
 
 
-@_where_it_lives
 def fp4_fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt="e4m3", sf_layout="rowmajor", out_dtype="f32", *,
-                       out=None) -> torch.Tensor:
+                       out=None, stream=None) -> torch.Tensor:
     """8-bit codes and scales back to fp32 or bf16 [rows, L]."""
+    dev = codes.get_device()
+    if stream is not None or dev < 0 or dev != _device():
+        return _elsewhere(fp4_fp8_dequantize, codes, stream, scales, fmt, sf_layout, out_dtype, out=out)
     f, sf, od = _FMT8[fmt], _SF[sf_layout], _OUT[out_dtype]
-    pitch = _codes8(codes, "codes")
+    pitch = _codes8(codes, dev, "codes")
     rows, cols = codes.shape
-    _same_device(codes, scales=scales, out=out)
-    _scales8(scales, rows, cols, sf, "scales")
-    dtype = torch.float32 if od == OUT_F32 else torch.bfloat16
+    sptr = _scales8(scales, dev, rows, cols, sf, "scales")
+    dtype = _f32 if od == OUT_F32 else _bf16
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+        out = codes.new_empty((rows, cols), dtype=dtype)
     else:
-        _contiguous(out, (rows, cols), dtype, "out")
-    _check(_lib.load().fp4_fp8_dequantize(codes.data_ptr(), pitch, scales.data_ptr(), rows, cols, f, sf, out.data_ptr(),
-                                          od, _stream(None)), "fp4_fp8_dequantize")
+        _fits(out, dev, dtype, (rows, cols), "out")
+    _check(_lib.load().fp4_fp8_dequantize(codes.data_ptr(), pitch, sptr, rows, cols, f, sf, out.data_ptr(), od,
+                                          _raw_stream(dev)), "fp4_fp8_dequantize")
     return out
 
 
-@_where_it_lives
 def fp4_fp8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
-                 a_fmt="e4m3", b_fmt="e4m3", out_dtype="bf16", *, out=None) -> torch.Tensor:
+                 a_fmt="e4m3", b_fmt="e4m3", out_dtype="bf16", *, out=None, stream=None) -> torch.Tensor:
     """Y[M, N] = A . B^T of block-scaled 8-bit operands [M, K] and [N, K] on the tensor cores (see fp4_fp8_gemm in
     include/fp4.h); scales in the tensor-core ("mma") layout.  With `out`, its dtype decides."""
+    dev = a_codes.get_device()
+    if stream is not None or dev < 0 or dev != _device():
+        return _elsewhere(fp4_fp8_gemm, a_codes, stream, a_scales, b_codes, b_scales, a_fmt, b_fmt, out_dtype, out=out)
     af, bf = _FMT8[a_fmt], _FMT8[b_fmt]
-    lda, ldb = _codes8(a_codes, "a_codes"), _codes8(b_codes, "b_codes")
+    lda, ldb = _codes8(a_codes, dev, "a_codes"), _codes8(b_codes, dev, "b_codes")
     M, K = a_codes.shape
-    N = b_codes.shape[0]
-    if b_codes.shape[1] != K:
+    N, kb = b_codes.shape
+    if kb != K:
         raise ValueError("A and B must have the same K")
-    _same_device(a_codes, a_scales=a_scales, b_codes=b_codes, b_scales=b_scales, out=out)
-    _scales8(a_scales, M, K, SF_MMA, "a_scales")
-    _scales8(b_scales, N, K, SF_MMA, "b_scales")
+    asp, bsp = _scales8(a_scales, dev, M, K, SF_MMA, "a_scales"), _scales8(b_scales, dev, N, K, SF_MMA, "b_scales")
     if out is None:
-        od = _OUT[out_dtype]
-        out = torch.empty((M, N), dtype=torch.float32 if od == OUT_F32 else torch.bfloat16, device=a_codes.device)
-    elif out.dtype not in (torch.float32, torch.bfloat16) or out.shape != (M, N) or (out.stride(1) != 1 and N != 1):
-        raise ValueError(f"out must be a bf16 or fp32 tensor of shape {(M, N)} with unit column stride")
-    _check(_lib.load().fp4_fp8_gemm(a_codes.data_ptr(), lda, a_scales.data_ptr(), b_codes.data_ptr(), ldb,
-                                    b_scales.data_ptr(), M, N, K, af, bf, out.data_ptr(), _row_stride(out),
-                                    _OUT[out.dtype], _stream(None)), "fp4_fp8_gemm")
+        od, ldy = _OUT[out_dtype], N
+        out = a_codes.new_empty((M, N), dtype=_f32 if od == OUT_F32 else _bf16)
+    else:
+        od, ldy = out.dtype, out.stride(0) if M != 1 else N
+        if od is not _bf16 and od is not _f32 or out.get_device() != dev or out.shape != (M, N) or \
+                (out.stride(1) != 1 and N != 1):
+            raise ValueError(f"out must be a bf16 or fp32 tensor of shape {(M, N)} with unit column stride on cuda:{dev}")
+        od = OUT_BF16 if od is _bf16 else OUT_F32
+    _check(_lib.load().fp4_fp8_gemm(a_codes.data_ptr(), lda, asp, b_codes.data_ptr(), ldb, bsp, M, N, K, af, bf,
+                                    out.data_ptr(), ldy, od, _raw_stream(dev)), "fp4_fp8_gemm")
     return out
 
 
-def _norm_weight(weight: torch.Tensor, cols: int) -> int:
-    if weight.dtype not in (torch.bfloat16, torch.float32) or weight.shape != (cols,) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous bf16 or fp32 tensor of shape ({cols},)")
-    return _OUT[weight.dtype]
+def _norm_weight(weight: torch.Tensor, dev: int, cols: int) -> int:
+    if weight.get_device() != dev or weight.dtype is not _bf16 and weight.dtype is not _f32 or \
+            weight.shape != (cols,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bf16 or fp32 tensor of shape ({cols},) on cuda:{dev}")
+    return OUT_BF16 if weight.dtype is _bf16 else OUT_F32
 
 
-@_where_it_lives
 def fp4_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
                              eps: float = 1e-6, fmt="e4m3", sf_layout="rowmajor", *, codes=None, scales=None,
-                             residual_out=None, rstd=None, norm_out=None) -> Fp8RmsNorm:
+                             residual_out=None, rstd=None, norm_out=None, stream=None) -> Fp8RmsNorm:
     """h = x + residual (bf16), y = h / sqrt(mean(h^2) + eps) * weight along the rows, y in 8-bit codes and scales,
     in one pass (see fp4_rmsnorm_fp8_quantize in include/fp4.h).  norm_out: a bf16 [rows, cols] tensor that
     receives y as well."""
+    dev = x.get_device()
+    if stream is not None or dev < 0 or dev != _device():
+        return _elsewhere(fp4_rmsnorm_fp8_quantize, x, stream, weight, residual, eps, fmt, sf_layout, codes=codes,
+                          scales=scales, residual_out=residual_out, rstd=rstd, norm_out=norm_out)
     _bf16_matrix(x)
     f, sf = _FMT8[fmt], _SF[sf_layout]
     rows, cols = shape = x.shape
-    _same_device(x, weight=weight, residual=residual, residual_out=residual_out, rstd=rstd, norm_out=norm_out)
-    wd = _norm_weight(weight, cols)
-    ldr = 0
+    wd = _norm_weight(weight, dev, cols)
+    ldr, rptr, hptr, yptr = 0, None, None, None
     if residual is not None:
-        ldr = _bf16_rows(residual, shape, "residual")
-        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device) if residual_out is None else \
-            _contiguous(residual_out, shape, torch.bfloat16, "residual_out")
+        ldr, rptr = _bf16_rows(residual, dev, shape, "residual"), residual.data_ptr()
+        if residual_out is None:
+            residual_out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+        else:
+            _fits(residual_out, dev, _bf16, shape, "residual_out")
+        hptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out is given without a residual")
-    rstd = torch.empty((rows,), dtype=torch.float32, device=x.device) if rstd is None else \
-        _contiguous(rstd, (rows,), torch.float32, "rstd")
+    if rstd is None:
+        rstd = x.new_empty((rows,), dtype=_f32)
+    else:
+        _fits(rstd, dev, _f32, (rows,), "rstd")
     if norm_out is not None:
-        _contiguous(norm_out, shape, torch.bfloat16, "norm_out")
-    codes, pitch, scales = _fp8_outputs(x, rows, cols, sf, codes, scales)
+        yptr = _fits(norm_out, dev, _bf16, shape, "norm_out").data_ptr()
+    codes, pitch, scales = _fp8_outputs(x, dev, rows, cols, sf, codes, scales)
     _check(_lib.load().fp4_rmsnorm_fp8_quantize(
-        x.data_ptr(), _row_stride(x), _ptr(residual), ldr, weight.data_ptr(), wd, rows, cols, eps, f, codes.data_ptr(),
-        pitch, scales.data_ptr(), sf, _ptr(residual_out), rstd.data_ptr(), _ptr(norm_out), _stream(None)),
+        x.data_ptr(), x.stride(0) if rows != 1 else cols, rptr, ldr, weight.data_ptr(), wd, rows, cols, eps, f,
+        codes.data_ptr(), pitch, scales.data_ptr(), sf, hptr, rstd.data_ptr(), yptr, _raw_stream(dev)),
         "fp4_rmsnorm_fp8_quantize")
     return Fp8RmsNorm(codes, scales, residual_out, rstd)
 
 
-@_where_it_lives
 def fp4_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
-                         dresidual: Optional[torch.Tensor] = None, *, dx=None, dweight=None, workspace=None):
+                         dresidual: Optional[torch.Tensor] = None, *, dx=None, dweight=None, workspace=None, stream=None):
     """Gradients of y = h * rstd * weight: (dx, the bf16 gradient of h -- of x and of residual alike -- plus
     `dresidual` where given, dweight in fp32).  See fp4_rmsnorm_backward in include/fp4.h."""
+    dev = dy.get_device()
+    if stream is not None or dev < 0 or dev != _device():
+        return _elsewhere(fp4_rmsnorm_backward, dy, stream, h, weight, rstd, dresidual, dx=dx, dweight=dweight,
+                          workspace=workspace)
     _bf16_matrix(dy, "dy")
     rows, cols = shape = dy.shape
-    _same_device(dy, h=h, weight=weight, rstd=rstd, dresidual=dresidual, dx=dx, dweight=dweight, workspace=workspace)
-    ldh, wd = _bf16_rows(h, shape, "h"), _norm_weight(weight, cols)
-    _contiguous(rstd, (rows,), torch.float32, "rstd")
-    lddr = 0 if dresidual is None else _bf16_rows(dresidual, shape, "dresidual")
-    dx = torch.empty(shape, dtype=torch.bfloat16, device=dy.device) if dx is None else \
-        _contiguous(dx, shape, torch.bfloat16, "dx")
-    dweight = torch.empty((cols,), dtype=torch.float32, device=dy.device) if dweight is None else \
-        _contiguous(dweight, (cols,), torch.float32, "dweight")
+    ldh, wd = _bf16_rows(h, dev, shape, "h"), _norm_weight(weight, dev, cols)
+    _fits(rstd, dev, _f32, (rows,), "rstd")
+    lddr, drptr = (0, None) if dresidual is None else (_bf16_rows(dresidual, dev, shape, "dresidual"), dresidual.data_ptr())
+    if dx is None:
+        dx = torch.empty_like(dy) if dy.is_contiguous() else dy.new_empty(shape)
+    else:
+        _fits(dx, dev, _bf16, shape, "dx")
+    if dweight is None:
+        dweight = dy.new_empty((cols,), dtype=_f32)
+    else:
+        _fits(dweight, dev, _f32, (cols,), "dweight")
     lib = _lib.load()
     if workspace is None:
         # an invalid shape needs 0 bytes: the call below refuses it
-        workspace = torch.empty((max(lib.fp4_rmsnorm_backward_workspace(rows, cols), 16),), dtype=torch.uint8,
-                                device=dy.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+        nbytes = lib.fp4_rmsnorm_backward_workspace(rows, cols)
+        workspace = dy.new_empty((nbytes or 16,), dtype=_u8)
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+        nbytes = workspace.numel() * workspace.element_size()
     _check(lib.fp4_rmsnorm_backward(
-        dy.data_ptr(), _row_stride(dy), h.data_ptr(), ldh, weight.data_ptr(), wd, rstd.data_ptr(), _ptr(dresidual), lddr,
-        rows, cols, dx.data_ptr(), dweight.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream(None)), "fp4_rmsnorm_backward")
+        dy.data_ptr(), dy.stride(0) if rows != 1 else cols, h.data_ptr(), ldh, weight.data_ptr(), wd, rstd.data_ptr(),
+        drptr, lddr, rows, cols, dx.data_ptr(), dweight.data_ptr(), workspace.data_ptr(), nbytes, _raw_stream(dev)),
+        "fp4_rmsnorm_backward")
     return dx, dweight
