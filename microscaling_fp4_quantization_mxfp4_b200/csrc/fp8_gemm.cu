@@ -397,14 +397,19 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
 
 }  // namespace tiles
 
-// ----------------------------------------------------- 256 x 256 over SM pairs --
-// A cluster of two CTAs on neighbouring SMs computes 256 x 256 of Y with M = 256, N = 256 MMAs issued by the
-// even CTA.  Each CTA stages its 128 rows of A, 128 of B's 256 rows and the scales of its A rows and of all
-// 256 B rows; both CTAs' loads signal the even CTA's barriers, whose MMA commits reach both.  At 96 bytes of
-// shared memory a clock and SM the operands stay below the 128 that it delivers, which 128-column tiles
-// would use up.  Persistent: one cluster an SM pair walks the tiles; the accumulator (256 columns; two would
-// leave no room for the scales) is free for the next tile as soon as its columns are in the eight epilogue
-// warps' registers, so only those loads, not the stores, stand between two tiles' MMAs.
+// ------------------------------------------------------ 256 x TN over SM pairs --
+// A cluster of two CTAs on neighbouring SMs computes 256 x TN of Y with M = 256, N = TN MMAs issued by the
+// even CTA.  Each CTA stages its 128 rows of A, half of B's TN rows and the scales of its A rows and of all B
+// rows; both CTAs' loads signal the even CTA's barriers, whose MMA commits reach both.  Persistent: one cluster
+// an SM pair walks the tiles.
+//
+// TN = 256: shared memory delivers 128 bytes a clock and SM; a block's operands, (128 + TN / 2) * 128 bytes, are
+// written to it once and read once, in the 2 TN cycles of its MMAs: all of it at 256, which wider tiles would
+// relieve and narrower ones overrun.  One accumulator (two would leave no columns for the scales); it is free
+// for the next tile as soon as its columns are in the epilogue warps' registers.
+// TN = 192: two accumulators, so that a tile is drained and stored while the next one is computed.  The 2700
+// cycles from a 256-column tile's last MMA to the next tile's first are as long as five blocks of K, and more
+// than the narrower tile's operands cost while K is short.
 //
 // warp 0 TMA producer, warp 1 MMA issuer, warps 2-9 epilogue, warp 10 scale copies.
 namespace pairs {
@@ -412,12 +417,21 @@ namespace pairs {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 96 + 32 * kEpiWarps;
 constexpr int kScaleWarp = 2 + kEpiWarps;
-constexpr int kOperand = 128 * kBK;                    // bytes of A, and of B, a CTA stages per block
-constexpr int kStageBytes = 2 * kOperand;
 constexpr int kScaleBytes = 3 * 512;                   // A's atom, B's two
-constexpr int kStages = (kRing - (int)kScaleBufs * kScaleBytes) / kStageBytes;
-constexpr int kSmem = 1024 + kStages * kStageBytes + (int)kScaleBufs * kScaleBytes + 512;
-constexpr uint32_t kScaleCol = 256, kScaleCols = 16;
+constexpr uint32_t kCols = 512, kScaleCols = 16;       // tensor memory columns, of them a scale buffer's
+constexpr int kStageRows = 2048;                       // bytes an epilogue warp passes its rows through
+
+template <int TN>
+struct Cfg {
+  static constexpr int kAccs = TN == 256 ? 1 : 2;
+  static constexpr int kA = 128 * kBK, kB = TN / 2 * kBK;        // bytes of A, and of B, a CTA stages per block
+  static constexpr int kStageBytes = kA + kB;
+  static constexpr int kFixed = (int)kScaleBufs * kScaleBytes + kEpiWarps * kStageRows + 512;
+  static constexpr int kStages = (226 * 1024 - 1024 - kFixed) / kStageBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kFixed;
+  static constexpr uint32_t kScaleCol = kAccs * TN;              // scale buffers behind the accumulators
+  static_assert((TN == 256 || TN == 192) && kScaleCol + kScaleBufs * kScaleCols <= kCols, "tile width");
+};
 
 __device__ __forceinline__ void fp8_mma_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                              uint32_t sfb, uint32_t accumulate) {
@@ -428,53 +442,75 @@ __device__ __forceinline__ void fp8_mma_pair(uint32_t d, uint64_t adesc, uint64_
       : "memory");
 }
 
-// 32 columns n0 .. n0 + 31 of one row.
-template <bool BF16>
-__device__ __forceinline__ void store32(const Fp8KernelArgs& p, const uint32_t (&r)[32], int m, int n0) {
-  const long long o = (long long)m * p.ldy + n0;
-  if (BF16) {
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + o;
-    if (p.vec_store && n0 + 32 <= p.N) {
+// 64 bytes' worth of columns of 32 rows of a tile from (m0, n0), lane = row: through 2 KB of shared memory (16-byte
+// piece j of row r at j ^ (r / 2 mod 4): no bank conflicts either way), so that four lanes store 64 contiguous
+// bytes of a row.  Measured against it: 16 bytes a lane straight from the registers (32 lines an instruction;
+// 50432 x 2304 x 768 136 against 93 us), 32 bytes a lane (96 us), TMA stores (92 us, but 2048 x 2048 x 512 8.0
+// against 7.6).  The columns are r[COL] on.
+template <bool BF16, int COL>
+__device__ __forceinline__ void store_rows(const Fp8KernelArgs& p, uint32_t stage, const uint32_t (&r)[32], int m0, int n0,
+                                           int lane) {
+  constexpr int kEl = BF16 ? 2 : 4, kPer = 16 / kEl;                // bytes of an element, elements of a piece
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint32_t w[4];
+  for (int j = 0; j < 4; ++j) {
+    uint4 v;
+    if (BF16) {
+      uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[8 * v + 2 * i]))) |
-                 ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[8 * v + 2 * i + 1]))) << 16);
-        reinterpret_cast<uint4*>(y)[v] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[8 * j + 2 * i]))) |
+               ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[8 * j + 2 * i + 1]))) << 16);
+      v = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (n0 + i < p.N) y[i] = __float2bfloat16_rn(__uint_as_float(r[i]));
+      v = make_uint4(r[COL + 4 * j], r[COL + 4 * j + 1], r[COL + 4 * j + 2], r[COL + 4 * j + 3]);
     }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+  }
+  __syncwarp();
+  const int piece = lane & 3, n = n0 + piece * kPer, row0 = lane >> 2;
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                 : "r"(stage + (row0 + 8 * i) * 64 + ((piece ^ ((row0 >> 1) & 3)) << 4))
+                 : "memory");
+  __syncwarp();
+  uint8_t* y = static_cast<uint8_t*>(p.y) + ((long long)(m0 + row0) * p.ldy + n) * kEl;
+  if (p.vec_store && n + kPer <= p.N) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (m0 + row0 + 8 * i < p.M) *reinterpret_cast<uint4*>(y + 8 * i * p.ldy * kEl) = v[i];
   } else {
-    float* y = static_cast<float*>(p.y) + o;
-    if (p.vec_store && n0 + 32 <= p.N) {
 #pragma unroll
-      for (int v = 0; v < 8; ++v)
-        reinterpret_cast<uint4*>(y)[v] = make_uint4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
-    } else {
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (n0 + i < p.N) y[i] = __uint_as_float(r[i]);
+      for (int e = 0; e < kPer; ++e)
+        if (n + e < p.N && m0 + row0 + 8 * i < p.M) {
+          if (BF16) reinterpret_cast<uint16_t*>(y + 8 * i * p.ldy * kEl)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+          else reinterpret_cast<uint32_t*>(y + 8 * i * p.ldy * kEl)[e] = w[e];
+        }
     }
   }
 }
 
-template <bool BF16>
+template <int TN, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                          const __grid_constant__ CUtensorMap tmap_sa, const __grid_constant__ CUtensorMap tmap_sb,
                          Fp8KernelArgs p) {
-  constexpr int S = kStages;
+  using C = Cfg<TN>;
+  constexpr int S = C::kStages;
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
-  uint8_t* sB = sA + S * kOperand;
-  uint8_t* sScale = sB + S * kOperand;
+  uint8_t* sB = sA + S * C::kA;
+  uint8_t* sOut = sB + S * C::kB;
+  uint8_t* sScale = sOut + kEpiWarps * kStageRows;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kScaleBufs * kScaleBytes);
   uint64_t* full = bars;
   uint64_t* empty = full + S;
@@ -482,10 +518,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* sfull = sload + kScaleBufs;                 // ... in tensor memory
   uint64_t* sempty = sfull + kScaleBufs;                // ... read by its last MMA
   uint64_t* tfull = sempty + kScaleBufs;
-  uint64_t* tempty = tfull + 1;
-  uint64_t* drain = tfull + 2;
-  uint64_t* sdrain = tfull + 3;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 4);
+  uint64_t* tempty = tfull + C::kAccs;
+  uint64_t* drain = tempty + C::kAccs;
+  uint64_t* sdrain = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sdrain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -505,8 +541,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sfull[b]), 1);
       mbar_init(smem_u32(&sempty[b]), 1);
     }
-    mbar_init(smem_u32(tfull), 1);
-    mbar_init(smem_u32(tempty), 2 * kEpiWarps);
+    for (int a = 0; a < C::kAccs; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), 2 * kEpiWarps);
+    }
     mbar_init(smem_u32(drain), 1);
     mbar_init(smem_u32(sdrain), 1);
     *abort_flag = 0;
@@ -550,8 +588,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t dst = smem_u32(sScale + b * kScaleBytes);
             if (leader) mbar_expect_tx(smem_u32(&sload[b]), 2u * (uint32_t)kScaleBytes);
             tma_load_2d_pair(dst, &tmap_sa, 0, (mt * 2 + (int)rank) * p.g4 + (kb >> 2), lb);
-            tma_load_2d_pair(dst + 512, &tmap_sb, 0, (nt * 2) * p.g4 + (kb >> 2), lb);
-            tma_load_2d_pair(dst + 1024, &tmap_sb, 0, (nt * 2 + 1) * p.g4 + (kb >> 2), lb);
+            const int atom = nt * TN / 128;                    // B's first atom (192: its rows may start in the middle)
+            tma_load_2d_pair(dst + 512, &tmap_sb, 0, atom * p.g4 + (kb >> 2), lb);
+            tma_load_2d_pair(dst + 1024, &tmap_sb, 0, (atom + 1) * p.g4 + (kb >> 2), lb);
           }
           if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
             raise_abort(abort_flag, p.error);
@@ -559,9 +598,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t fb = map_rank(smem_u32(&full[stage]), 0);
-          if (leader) mbar_expect_tx(smem_u32(&full[stage]), 2u * (uint32_t)kStageBytes);
-          tma_load_2d_pair(smem_u32(sA + stage * kOperand), &tmap_a, kb * kBK, mt * 256 + (int)rank * 128, fb);
-          tma_load_2d_pair(smem_u32(sB + stage * kOperand), &tmap_b, kb * kBK, nt * 256 + (int)rank * 128, fb);
+          if (leader) mbar_expect_tx(smem_u32(&full[stage]), 2u * (uint32_t)C::kStageBytes);
+          tma_load_2d_pair(smem_u32(sA + stage * C::kA), &tmap_a, kb * kBK, mt * 256 + (int)rank * 128, fb);
+          tma_load_2d_pair(smem_u32(sB + stage * C::kB), &tmap_b, kb * kBK, nt * TN + (int)rank * (TN / 2), fb);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -577,12 +616,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, ns = 0, local = 0;
       bool ok = true, any_mma = false;
       for (int t = cluster; t < num_tiles && ok; t += nclusters, ++local) {
-        if (!wait_spin(smem_u32(tempty), (local & 1u) ^ 1u, abort_flag)) {
+        const uint32_t acc = local % C::kAccs;
+        if (!wait_spin(smem_u32(&tempty[acc]), ((local / C::kAccs) & 1u) ^ 1u, abort_flag)) {
           raise_abort(abort_flag, p.error);
           ok = false;
           break;
         }
         tc_fence_after();
+        const uint32_t d = tmem + acc * TN;
+        int mt, nt;
+        tile_coords(t, p.num_m, p.num_n, mt, nt);
+        const uint32_t sb_off = 4u + (((uint32_t)(nt * TN) >> 5) & 3u);       // B's first row in its atom, 32 a column
         for (int kb = 0; kb < nkb; ++kb) {
           if ((kb & 3) == 0) {
             if (!wait_spin(smem_u32(&sfull[ns % kScaleBufs]), (ns / kScaleBufs) & 1u, abort_flag)) {
@@ -599,13 +643,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t b = (ns - 1) % kScaleBufs;
-          const uint32_t sa = tmem + kScaleCol + b * kScaleCols, sb = sa + 4u;
-          const uint64_t adesc = desc_sw128(smem_u32(sA + stage * kOperand));
-          const uint64_t bdesc = desc_sw128(smem_u32(sB + stage * kOperand));
-          const uint32_t idesc = fp8_idesc(256, 256, p.a_type, p.b_type, (uint32_t)(kb & 3));
+          const uint32_t sa = tmem + C::kScaleCol + b * kScaleCols, sb = sa + sb_off;
+          const uint64_t adesc = desc_sw128(smem_u32(sA + stage * C::kA));
+          const uint64_t bdesc = desc_sw128(smem_u32(sB + stage * C::kB));
+          const uint32_t idesc = fp8_idesc(256, TN, p.a_type, p.b_type, (uint32_t)(kb & 3));
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            fp8_mma_pair(tmem, adesc + (uint64_t)(2 * j), bdesc + (uint64_t)(2 * j), idesc, sa, sb,
+            fp8_mma_pair(d, adesc + (uint64_t)(2 * j), bdesc + (uint64_t)(2 * j), idesc, sa, sb,
                          (kb > 0 || j > 0) ? 1u : 0u);
           any_mma = true;
           tc_commit_pair(smem_u32(&empty[stage]));
@@ -616,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        tc_commit_pair(smem_u32(tfull));
+        tc_commit_pair(smem_u32(&tfull[acc]));
       }
       if (!ok && any_mma) {
         // the MMAs already issued end before tensor memory is released
@@ -641,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = tmem + kScaleCol + b * kScaleCols;
+          const uint32_t sa = tmem + C::kScaleCol + b * kScaleCols;
 #pragma unroll
           for (int i = 0; i < 3; ++i)
             tc_cp_sf_pair(sa + 4u * i, desc_sf(smem_u32(sScale + b * kScaleBytes + 512 * i)));
@@ -658,37 +702,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue --
-    // warp w: tensor-memory lanes 32 * (w % 4) .. + 31 and 128 of the 256 columns
+    // warp w: tensor-memory lanes 32 * (w % 4) .. + 31 and half of the tile's columns
     const int q = warp & 3;
-    const int col0 = ((warp - 2) / 4) * 128;
+    const int col0 = ((warp - 2) / 4) * (TN / 2);
+    const uint32_t stage = smem_u32(sOut + (warp - 2) * kStageRows);
     const uint32_t tempty_leader = map_rank(smem_u32(tempty), 0);
     uint32_t local = 0;
     for (int t = cluster; t < num_tiles; t += nclusters, ++local) {
       int mt, nt;
       tile_coords(t, p.num_m, p.num_n, mt, nt);
+      const uint32_t acc = local % C::kAccs;
       int ok = 1;
-      if (lane == 0) ok = wait_bounded(smem_u32(tfull), local & 1u, abort_flag) ? 1 : 0;
+      if (lane == 0) ok = wait_bounded(smem_u32(&tfull[acc]), (local / C::kAccs) & 1u, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok) {
         if (lane == 0) raise_abort(abort_flag, p.error);
         break;
       }
       tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)col0;
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + acc * TN + (uint32_t)col0;
       uint32_t r[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tbase + (uint32_t)(32 * c), r[c]);
+      for (int c = 0; c < 4; ++c) {
+        if (c < TN / 64) {
+          tmem_ld32(tbase + (uint32_t)(32 * c), r[c]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[c][i] = 0u;
+        }
+      }
       tmem_ld_wait(r);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty_leader);
-      const int m = mt * 256 + (int)rank * 128 + q * 32 + lane;
-      if (m < p.M) {
+      if (lane == 0) mbar_arrive_remote(tempty_leader + 8u * acc);
+      const int m0 = mt * 256 + (int)rank * 128 + q * 32, n0 = nt * TN + col0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n0 = nt * 256 + col0 + 32 * c;
-          if (n0 < p.N) store32<BF16>(p, r[c], m, n0);
-        }
+      for (int c = 0; c < TN / 64; ++c) {
+        store_rows<BF16, 0>(p, stage, r[c], m0, n0 + 32 * c, lane);
+        if (!BF16) store_rows<BF16, 16>(p, stage, r[c], m0, n0 + 32 * c + 16, lane);
       }
     }
   }
@@ -799,34 +850,45 @@ bool scale_map(CUtensorMap* map, const uint8_t* base, int64_t atoms) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool BF16>
+template <int TN, bool BF16>
 cudaError_t run_pairs(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
-  static_assert(pairs::kStages >= 2 && pairs::kSmem <= 227 * 1024, "shared memory");
-  auto kernel = pairs::fp8_gemm_pair_kernel<BF16>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, pairs::kSmem);
+  using C = pairs::Cfg<TN>;
+  static_assert(C::kStages >= 2 && C::kSmem <= 227 * 1024, "shared memory");
+  auto kernel = pairs::fp8_gemm_pair_kernel<TN, BF16>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
   Fp8KernelArgs p = kernel_args(q);
   CUtensorMap ta, tb, tsa, tsb;
   if (!code_map(&ta, q.a, q.M, q.K, q.lda, 128)) return cudaErrorNotSupported;
-  if (!code_map(&tb, q.b, q.N, q.K, q.ldb, 128)) return cudaErrorNotSupported;
+  if (!code_map(&tb, q.b, q.N, q.K, q.ldb, TN / 2)) return cudaErrorNotSupported;
   if (!scale_map(&tsa, q.a_sf, (q.M + 127) / 128 * p.g4)) return cudaErrorNotSupported;
   if (!scale_map(&tsb, q.b_sf, (q.N + 127) / 128 * p.g4)) return cudaErrorNotSupported;
   p.num_m = (int)((q.M + 255) / 256);
-  p.num_n = (int)((q.N + 255) / 256);
+  p.num_n = (int)((q.N + TN - 1) / TN);
   const int clusters = std::min(num_sms / 2, p.num_m * p.num_n);
-  return launch_kernel(kernel, dim3(2 * clusters), dim3(pairs::kThreads), pairs::kSmem, st, false, 1u, ta, tb, tsa, tsb, p);
+  return launch_kernel(kernel, dim3(2 * clusters), dim3(pairs::kThreads), C::kSmem, st, false, 1u, ta, tb, tsa, tsb, p);
 }
 
 template <bool BF16>
 cudaError_t dispatch(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
+  // Up to 128 rows of A: tiles of Y^T stream B over every SM (128 x 4096 x 4096: 10.1 against 12.8 us), unless more than
+  // half of them would be there for more than 64 rows (128 x 11008 x 4096: 15.5 against 14.6 us).
+  if (q.M > 128 || (q.M > 64 && 2 * ((q.N + 127) / 128) > num_sms)) {
+    const int64_t num_m = (q.M + 255) / 256, narrow = num_m * ((q.N + 191) / 192), wide = num_m * ((q.N + 255) / 256);
+    const int64_t pairs = num_sms / 2, narrow_waves = (narrow + pairs - 1) / pairs, wide_waves = (wide + pairs - 1) / pairs;
+    // Few tiles and a long K: K divided over clusters (256 x 1024 x 8192, 6 tiles: 12.7 against 19.1 us; 512 x 1024 x
+    // 4096, 12 tiles: 11.7 against 12.0; 256 x 4096 x 4096, 22 tiles: 13.8 against 13.0).
+    if (8 * narrow <= num_sms && q.K >= 4096) return run_tiles<256, BF16>(q, num_sms, st);
+    // A wave of 192 columns takes 0.70 to 0.78 of one of 256 from K = 1536 on and 0.80 to 0.84 at 768 (8192 x 11008 x
+    // 4096: 26 waves in 257 us against 19 in 260; 4096 x 4096 x 2048: 5 in 27.9 against 4 in 30.4; 50432 x 2304 x 768:
+    // 32 in 99.7 against 24 in 93.4).
+    if ((q.K >= 1536 ? 75 : 82) * narrow_waves <= 100 * wide_waves) return run_pairs<192, BF16>(q, num_sms, st);
+    return run_pairs<256, BF16>(q, num_sms, st);
+  }
   if (q.M <= 16) return run_tiles<16, BF16>(q, num_sms, st);
   if (q.M <= 32) return run_tiles<32, BF16>(q, num_sms, st);
   if (q.M <= 64) return run_tiles<64, BF16>(q, num_sms, st);
-  if (q.M <= 128) return run_tiles<128, BF16>(q, num_sms, st);
-  // 256 x 256 tiles for at least a quarter of the SM pairs; fewer leave the device idle, and K divided over
-  // clusters is faster (256 x 4096 x 4096, 16 tiles: 13.6 against 16.8 us; 512 rows, 32 tiles: 18.2 against 17.2)
-  if (8 * ((q.M + 255) / 256) * ((q.N + 255) / 256) >= num_sms) return run_pairs<BF16>(q, num_sms, st);
-  return run_tiles<256, BF16>(q, num_sms, st);
+  return run_tiles<128, BF16>(q, num_sms, st);
 }
 
 }  // namespace
