@@ -881,8 +881,10 @@ cudaError_t dispatch(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
     if (8 * narrow <= num_sms && q.K >= 4096) return run_tiles<256, BF16>(q, num_sms, st);
     // A wave of 192 columns takes 0.70 to 0.78 of one of 256 from K = 1536 on and 0.80 to 0.84 at 768 (8192 x 11008 x
     // 4096: 26 waves in 257 us against 19 in 260; 4096 x 4096 x 2048: 5 in 27.9 against 4 in 30.4; 50432 x 2304 x 768:
-    // 32 in 99.7 against 24 in 93.4).
-    if ((q.K >= 1536 ? 75 : 82) * narrow_waves <= 100 * wide_waves) return run_pairs<192, BF16>(q, num_sms, st);
+    // 32 in 99.7 against 24 in 93.4).  Rows that start between 32-byte sectors cost a load a fifth sector, and narrow
+    // tiles load more (4096 x 4096 x 8201 in rows of 8208 bytes: 5 waves in 151 us against 4 in 142).
+    const bool sectors = q.lda % 32 == 0 && q.ldb % 32 == 0;
+    if ((q.K >= 1536 && sectors ? 75 : 82) * narrow_waves <= 100 * wide_waves) return run_pairs<192, BF16>(q, num_sms, st);
     return run_pairs<256, BF16>(q, num_sms, st);
   }
   if (q.M <= 16) return run_tiles<16, BF16>(q, num_sms, st);

@@ -8,7 +8,8 @@
 //   g = dy * weight, xh = h * rstd, c = mean(g * xh)
 //   dx = rstd * (g - xh * c) + dresidual,  dweight = sum over rows of dy * xh
 //
-// Sums, statistics and y are fp32; the only roundings to fewer bits are the outputs' own.
+// Sums and statistics are fp32 or wider (the rows' sums of squares and rstd in fp64, at no cost in time), y is fp32;
+// the only roundings to fewer bits are the outputs' own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -56,12 +57,28 @@ __device__ __forceinline__ float row_sum(float v, float* part, uint32_t first_wa
   return v;
 }
 
+// The same of fp64 values.
+template <bool WARP>
+__device__ __forceinline__ double row_sum64(double v, double* part, uint32_t first_warp, uint32_t warps) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  if (!WARP) {
+    const uint32_t lane = threadIdx.x & 31u;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < warps ? part[first_warp + lane] : 0.0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  }
+  return v;
+}
+
 struct NormArgs {
   const uint16_t* x;
   const uint16_t* residual;
   const void* weight;
   long long rows, ldx, ldr, ldc;
-  float eps, fcols;
+  double eps, inv_cols;
   uint8_t* codes;
   uint8_t* scales;
   uint16_t* residual_out;
@@ -81,7 +98,7 @@ constexpr int kShortThreads = 256;
 template <int FMT, int CPT, int MOST, int BLOCKS>
 __global__ void __launch_bounds__(MOST, BLOCKS) rmsnorm_fp8_kernel(NormArgs p) {
   constexpr bool WARP = MOST == kShortThreads;
-  __shared__ float part[32];
+  __shared__ double part[32];
   pdl_trigger();
   const uint32_t TPR = WARP ? 32u : p.tpr;
   const uint32_t slot = WARP ? threadIdx.x >> 5 : threadIdx.x / TPR, t = threadIdx.x - slot * TPR;
@@ -101,7 +118,6 @@ __global__ void __launch_bounds__(MOST, BLOCKS) rmsnorm_fp8_kernel(NormArgs p) {
     h[k] = make_uint4(0, 0, 0, 0);
     if (on[k]) h[k] = *reinterpret_cast<const uint4*>(x + k * TPR * 8);
   }
-  float2 s2 = make_float2(0.0f, 0.0f);
   if (p.residual != nullptr) {
     uint4 r[CPT];
     const uint16_t* res = p.residual + row * p.ldr + t * 8;
@@ -123,15 +139,22 @@ __global__ void __launch_bounds__(MOST, BLOCKS) rmsnorm_fp8_kernel(NormArgs p) {
       if (on[k]) *reinterpret_cast<uint4*>(out + k * TPR * 8) = h[k];
     }
   }
+  // a chunk's squares in fp32, the chunks' and threads' sums in fp64
+  double chunk_sums = 0.0;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     float2 a[4];
     unpack2(h[k], a);
+    float2 s2 = fp4dev::mul2(a[0], a[0]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s2 = __ffma2_rn(a[i], a[i], s2);
+    for (int i = 1; i < 4; ++i) s2 = __ffma2_rn(a[i], a[i], s2);
+    chunk_sums = __dadd_rn(chunk_sums, (double)__fadd_rn(s2.x, s2.y));
   }
-  const float ss = row_sum<WARP>(__fadd_rn(s2.x, s2.y), part, slot * (TPR / 32), TPR / 32);
-  const float rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, p.fcols), p.eps));
+  const double ss = row_sum64<WARP>(chunk_sums, part, slot * (TPR / 32), TPR / 32);
+  // 1 / sqrt(mean + eps), the fp32 root and one Newton step in fp64
+  const double ms = __fma_rn(ss, p.inv_cols, p.eps), r0 = (double)__frsqrt_rn((float)ms);
+  const double fix = __dmul_rn(__dmul_rn(0.5, r0), __fma_rn(-__dmul_rn(ms, r0), r0, 1.0));
+  const float rstd = (float)(isfinite(fix) ? __dadd_rn(r0, fix) : r0);
   if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
   const float2 r2 = make_float2(rstd, rstd);
   float2 y[CPT][4];
@@ -528,8 +551,8 @@ cudaError_t launch_rmsnorm_fp8(const RmsNormParams& q, int num_sms, cudaStream_t
   p.ldx = q.ldx;
   p.ldr = q.ldr;
   p.ldc = q.ldc;
-  p.eps = q.eps;
-  p.fcols = (float)q.cols;
+  p.eps = (double)q.eps;
+  p.inv_cols = 1.0 / (double)q.cols;
   p.codes = q.codes;
   p.scales = q.scales;
   p.residual_out = static_cast<uint16_t*>(q.residual_out);
