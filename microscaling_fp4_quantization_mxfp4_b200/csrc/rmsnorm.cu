@@ -375,24 +375,23 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[k][i] = make_float2(v[2 * i], v[2 * i + 1]);
     }
-  const float* rs = p.rstd + blockIdx.x;
   uint16_t* out = p.dx + (long long)blockIdx.x * p.cols + t * 8;
   const long long out_step = (long long)gridDim.x * p.cols;
-  float nrstd[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) nrstd[r] = r < count ? rs[(long long)r * gridDim.x] : 0.0f;
+  // rstd of 32 rows a lane each, and of the 32 behind them: a load for each row, one row ahead, was what rows waited for
+  auto rstd_of = [&](int n) { return n < count ? p.rstd[blockIdx.x + (long long)n * gridDim.x] : 0.0f; };
+  float rs = rstd_of((int)lane), rs_next = rstd_of(32 + (int)lane);
   bool late = false;
   int slot = 0;
   uint32_t phase = 0;
   for (int n0 = 0, flip = 0; n0 < count; n0 += R, flip ^= 1) {
     float rstd[R], sum[R];
     uint32_t at[R];                                            // the rows' slots
-    rs += (long long)R * gridDim.x;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      rstd[r] = nrstd[r];
-      nrstd[r] = n0 + R + r < count ? rs[(long long)r * gridDim.x] : 0.0f;
+    if ((n0 & 31) == 0 && n0 > 0) {
+      rs = rs_next;
+      rs_next = rstd_of(n0 + 32 + (int)lane);
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r) rstd[r] = __shfl_sync(0xFFFFFFFFu, rs, (n0 + r) & 31);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       sum[r] = 0.0f;
