@@ -575,6 +575,7 @@ fp4_status fp4_fp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_sf, cons
   constexpr int64_t kMost = ((int64_t)1 << 31) - 4096;
   if (M > kMost || N > kMost || K > kMost || lda >= (int64_t)1 << 40 || ldb >= (int64_t)1 << 40) return FP4_ERR_SHAPE;
   if (((M + 127) / 128) * ((N + 127) / 128) >= kMost / 8) return FP4_ERR_SHAPE;
+  if (((M > N ? M : N) + 255) / 128 * ((K + 511) / 512) >= kMost) return FP4_ERR_SHAPE;       // scale atoms
   if (!aligned16(a_sf) || !aligned16(b_sf)) return FP4_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(y) & (y_dtype == FP4_OUT_F32 ? 3u : 1u)) != 0) return FP4_ERR_ALIGN;
   DeviceState* d = nullptr;

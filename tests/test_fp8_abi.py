@@ -72,6 +72,10 @@ def test_gemm_refusals(lib):
             (9, 2, ARG), (10, -1, ARG), (11, None, ARG), (11, FAKE + 1, ALIGN), (12, 7, ARG), (13, 2, ARG),
             (6, 1 << 31, SHAPE)]):
         assert lib.fp4_fp8_gemm(*args) == status, args
+    # scale atoms, 128 rows x 512 elements of K, are counted in 32 bits
+    big = list(good)
+    big[1], big[4], big[6], big[8] = 1 << 26, 1 << 26, 1 << 22, 1 << 26
+    assert lib.fp4_fp8_gemm(*big) == SHAPE
     assert lib.fp4_fp8_gemm(*good[:11], FAKE + 2, 8, 0, None) == ALIGN          # fp32 output on a 2-byte boundary
 
 

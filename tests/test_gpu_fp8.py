@@ -161,6 +161,16 @@ def test_gemm_large(M, N, K):
     _check_gemm(M, N, K, seed=7)
 
 
+@pytest.mark.parametrize("M, N, K, ldy", [
+    (130, 300, 5000, 304), (300, 513, 4100, 513),        # few tiles, long K: K over clusters, more than 128 rows
+    (2048, 2304, 768, 2304), (1500, 2000, 300, 2001),    # 256 x 256 tiles
+    (513, 1000, 1016, 1008), (257, 200, 1600, 201),      # 256 x 192 tiles, rows of codes 16 bytes off a sector
+    (96, 9600, 256, 9600), (128, 9501, 520, 9501),       # 65 to 128 rows against many weights
+    (40, 9600, 300, 9600), (16, 20000, 264, 20000)])     # one CTA a tile, more tiles than SMs
+def test_gemm_kernels(M, N, K, ldy):
+    _check_gemm(M, N, K, "e5m2", "e4m3", seed=8, ldy=ldy)
+
+
 @pytest.mark.parametrize("M", [1, 40, 700])
 def test_gemm_nan_blocks_reach_their_rows_only(M):
     a, sa, av = _operand(M, 300, "e4m3", 1)
@@ -180,6 +190,38 @@ def test_gemm_repeats_bit_for_bit(M, N, K):
     first = fp.fp4_fp8_gemm(a, sa, b, sb, out_dtype="f32")
     for _ in range(3):
         assert torch.equal(fp.fp4_fp8_gemm(a, sa, b, sb, out_dtype="f32"), first)
+
+
+def test_offsets_past_32_bits():
+    """2.4e9 elements: the last rows (and columns, along axis 0) are those of the same rows on their own."""
+    rows, cols = 600_040, 4096
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for i in range(0, rows, 65536):
+        x[i:i + 65536] = torch.randn(min(65536, rows - i), cols, generator=g, device="cuda").to(torch.bfloat16)
+    last = (rows - 1) // 128 * 128 - 128                            # a whole and a partial block of 128 rows
+    part = x[last:].clone()
+    q = fp.fp4_fp8_quantize(x, sf_layout="mma")
+    p = fp.fp4_fp8_quantize(part, sf_layout="mma")
+    assert torch.equal(q.codes[last:], p.codes) and torch.equal(q.scales[-p.scales.numel():], p.scales)
+    w = torch.randn(24, cols, generator=g, device="cuda").to(torch.bfloat16)
+    wq = fp.fp4_fp8_quantize(w, sf_layout="mma")
+    y = fp.fp4_fp8_gemm(q.codes, q.scales, wq.codes, wq.scales, out_dtype="f32")
+    z = fp.fp4_fp8_gemm(wq.codes, wq.scales, q.codes, q.scales, out_dtype="f32")
+    a = fp.fp4_fp8_dequantize(p.codes, p.scales, "e4m3", "mma").double()
+    b = fp.fp4_fp8_dequantize(wq.codes, wq.scales, "e4m3", "mma").double()
+    tol = _bound(cols, (a.abs() @ b.abs().t()).cpu().numpy())
+    assert np.all((y[last:].double() - a @ b.t()).abs().cpu().numpy() <= tol)
+    assert np.all((z[:, last:].t().double() - a @ b.t()).abs().cpu().numpy() <= tol)
+    del q, y, z
+    q, p = fp.fp4_fp8_quantize(x, axis=0), fp.fp4_fp8_quantize(part, axis=0)
+    assert torch.equal(q.codes[:, last:], p.codes) and torch.equal(q.scales[:, -2:], p.scales)
+    del q
+    n, m = fp.fp4_rmsnorm_fp8_quantize(x, w[0], x), fp.fp4_rmsnorm_fp8_quantize(part, w[0], part)
+    assert torch.equal(n.codes[last:], m.codes) and torch.equal(n.residual_out[last:], m.residual_out)
+    assert torch.equal(n.rstd[last:], m.rstd)
+    dx = fp.fp4_rmsnorm_backward(x, n.residual_out, w[0], n.rstd, x, dx=n.residual_out)[0]
+    assert torch.equal(dx[last:], fp.fp4_rmsnorm_backward(part, m.residual_out, w[0], m.rstd, part)[0])
 
 
 def test_streams_and_graphs():
