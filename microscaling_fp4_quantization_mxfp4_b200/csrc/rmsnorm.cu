@@ -40,24 +40,13 @@ __device__ __forceinline__ void load_weight8(const void* w, int f32, uint32_t ch
   }
 }
 
-// Sum over the `warps` warps of a row (every thread of the block takes part; `part` holds one float per
-// warp of the block).  Within the warp, then over the row's warps, in a fixed order.
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float* part, uint32_t first_warp, uint32_t warps) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  if (!WARP) {
-    const uint32_t lane = threadIdx.x & 31u;
-    if (lane == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < warps ? part[first_warp + lane] : 0.0f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  }
   return v;
 }
-
-// The same of fp64 values.
+// Sum over the `warps` warps of a row (every thread of the block takes part; `part` holds one value per warp of
+// the block).  Within the warp, then over the row's warps, in a fixed order.  WARP: the row is one warp's.
 template <bool WARP>
 __device__ __forceinline__ double row_sum64(double v, double* part, uint32_t first_warp, uint32_t warps) {
 #pragma unroll
@@ -91,7 +80,9 @@ struct NormArgs {
 
 // tpr threads a row, CPT 8-element chunks a thread: the row stays in registers between the sum of
 // squares and the quantization, so x and the residual are read once.  Bound by HBM (7 bytes an element
-// with a residual); one row of few: by the latency of load -> sum -> store.  Rows of up to 1024 elements are one
+// with a residual; 16384 x 4096: 76 us, 0.96 of the copy rate); one row of few: by the latency of load -> sum ->
+// store (2.6 us).  Two chunks a thread took 91 us, eight 122: a row's fixed work (some 150 instructions a thread) is
+// spread over more elements, until the registers leave too few rows in flight.  Rows of up to 1024 elements are one
 // warp's, eight a block, and nothing waits for another warp.  MOST, BLOCKS: threads of a block, blocks an SM;
 // three blocks of up to 384 threads (56 registers) against two took 4096 x 11008 from 70.7 to 59.9 us.
 constexpr int kShortThreads = 256;
@@ -225,7 +216,8 @@ __device__ __forceinline__ void store_partials(const NormBwdArgs& p, const float
 }
 
 // Rows of up to 1024 elements: a warp a row, eight rows a block.  A warp walks its rows with the next one's
-// loads issued before this one's sum and keeps its columns' sums of dy * xh in registers.
+// loads issued before this one's sum and keeps its columns' sums of dy * xh in registers.  Bound by HBM (50432 x 768
+// with a residual: 58 us, 0.83 of the copy rate; rows over 64 threads with a barrier each took 125).
 template <int CPT>
 __global__ void __launch_bounds__(256, 2) rmsnorm_backward_short_kernel(NormBwdArgs p) {
   extern __shared__ float2 slot_sums[];             // [7][4][chunks]
@@ -285,9 +277,9 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_backward_short_kernel(NormBwdA
         }
       }
     }
-    const float sum = row_sum<true>(__fadd_rn(s2.x, s2.y), nullptr, 0, 1);
-    // dx = g * rstd + (h * (-rstd^2 * c) + dresidual)
-    const float kf = __fmul_rn(__fmul_rn(-r2.x, r2.x), __fmul_rn(sum, p.inv_cols));
+    const float sum = warp_sum(__fadd_rn(s2.x, s2.y));
+    // dx = g * rstd + (xh * (-rstd * c) + dresidual)
+    const float kf = __fmul_rn(-r2.x, __fmul_rn(sum, p.inv_cols));
     const float2 k2 = make_float2(kf, kf);
 #pragma unroll
     for (int k = 0; k < CPT; ++k) {
@@ -302,7 +294,8 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_backward_short_kernel(NormBwdA
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = __ffma2_rn(__fmul2_rn(a[i], make_float2(w[2 * i], w[2 * i + 1])), r2, __ffma2_rn(b[i], k2, e[i]));
+          const float2 v = __ffma2_rn(__fmul2_rn(a[i], make_float2(w[2 * i], w[2 * i + 1])), r2,
+                                      __ffma2_rn(__fmul2_rn(b[i], r2), k2, e[i]));
           o[i] = pack_bf16(v.x, v.y);
         }
         *reinterpret_cast<uint4*>(p.dx + row * p.cols + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -326,12 +319,13 @@ __global__ void __launch_bounds__(256, 2) rmsnorm_backward_short_kernel(NormBwdA
   store_partials<CPT>(p, acc, t, 32);
 }
 
-// Longer rows: a block takes R rows at a time, CPT chunks a thread.  Rows arrive in a ring of shared-memory
+// Longer rows: a block takes R rows at a time, CPT = 2 chunks a thread.  Rows arrive in a ring of shared-memory
 // slots by bulk copies (one an array), so that what is in flight takes no registers, and are read from there
 // twice, for the sum and for dx.  The sums of R rows share one barrier; behind it every thread has read the
 // previous R rows, and their slots are filled again.  What a row costs a thread besides its elements (waits,
 // shuffles, addresses: some 60 instructions) is why a thread takes 16 elements of it and not 8, and the
-// arithmetic runs on packed pairs.
+// arithmetic runs on packed pairs.  Bound by HBM (16384 x 4096 with a residual: 93 us, 0.90 of the copy rate; a block
+// a row with everything in registers took 106, eight elements a thread 155).
 template <int R>
 __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs p, int ring_rows, unsigned* error) {
   constexpr int CPT = 2;
@@ -443,8 +437,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (n0 + r < count) {
-        // dx = g * rstd + (h * (-rstd^2 * c) + dresidual)
-        const float kf = __fmul_rn(__fmul_rn(-rstd[r], rstd[r]), __fmul_rn(sum[r], p.inv_cols));
+        // dx = g * rstd + (xh * (-rstd * c) + dresidual)
+        const float kf = __fmul_rn(-rstd[r], __fmul_rn(sum[r], p.inv_cols));
         const float2 r2 = make_float2(rstd[r], rstd[r]), k2 = make_float2(kf, kf);
 #pragma unroll
         for (int k = 0; k < CPT; ++k) {
@@ -461,7 +455,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 v = __ffma2_rn(__fmul2_rn(a[i], w[k][i]), r2, __ffma2_rn(b[i], k2, e[i]));
+              const float2 v = __ffma2_rn(__fmul2_rn(a[i], w[k][i]), r2, __ffma2_rn(__fmul2_rn(b[i], r2), k2, e[i]));
               o[i] = pack_bf16(v.x, v.y);
             }
             *reinterpret_cast<uint4*>(out + k * TPR * 8) = make_uint4(o[0], o[1], o[2], o[3]);

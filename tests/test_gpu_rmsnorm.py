@@ -168,6 +168,19 @@ def test_backward_in_place():
         assert torch.equal(fp.fp4_rmsnorm_backward(t[0], t[1], w, rstd, t[2], dx=t[i])[0], want)
 
 
+def test_backward_of_tiny_rows():
+    """eps = 0 and rows near 1e-20: rstd squared is past fp32, dx is not."""
+    h, dy = _rand(3, 264, 1, 1e-20), _rand(3, 264, 2, 1e-3)
+    rstd = torch.from_numpy(fp8.rmsnorm(_f64(h), np.ones(264), 0.0)[1]).float().cuda()
+    dx, dw = fp.fp4_rmsnorm_backward(dy, h, torch.ones(264, device="cuda"), rstd)
+    want, wantw = fp8.rmsnorm_backward(_f64(dy), _f64(h), np.ones(264), rstd.double().cpu().numpy())
+    r = rstd.double().cpu().numpy()[:, None]
+    g, xh = np.abs(_f64(dy)), np.abs(_f64(h) * r)
+    err = (264 + 16) * U * r * (g + xh * (g * xh).mean(axis=1, keepdims=True))
+    assert np.all(np.abs(_f64(dx) - want) <= err + 2.0 ** -8 * (np.abs(want) + err))
+    assert np.all(np.abs(dw.double().cpu().numpy() - wantw) <= 7 * U * (g * xh).sum(axis=0))
+
+
 def test_two_graphs_share_nothing():
     """Norm and backward captured twice and replayed in turn on new inputs give the plain calls' bits."""
     w = torch.ones(1032, device="cuda")
