@@ -839,7 +839,8 @@ cudaError_t run_tiles(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
   using C = tiles::Cfg<BNT>;
   static_assert(C::kStages >= 2 && C::kSmem <= 227 * 1024, "shared memory");
   auto kernel = tiles::fp8_gemm_tile_kernel<BNT, BF16>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static SmemLimit limit;
+  const cudaError_t attr = limit.raise(kernel, C::kSmem);
   if (attr != cudaSuccess) return attr;
   CUtensorMap tw, tx;
   if (!code_map(&tw, q.b, q.N, q.K, q.ldb, 128)) return cudaErrorNotSupported;
@@ -874,7 +875,8 @@ cudaError_t run_pairs(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
   using C = pairs::Cfg<TN>;
   static_assert(C::kStages >= 2 && C::kSmem <= 227 * 1024, "shared memory");
   auto kernel = pairs::fp8_gemm_pair_kernel<TN, BF16>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static SmemLimit limit;
+  const cudaError_t attr = limit.raise(kernel, C::kSmem);
   if (attr != cudaSuccess) return attr;
   Fp8KernelArgs p = kernel_args(q);
   CUtensorMap ta, tb, tsa, tsb;

@@ -5,7 +5,30 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fp4lib {
+
+// Raises a kernel's limit of dynamic shared memory, once a device: a function's attributes are each device's
+// own.  One object a kernel.
+class SmemLimit {
+ public:
+  template <typename K>
+  cudaError_t raise(K* kernel, int bytes) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < kDevices;
+    if (kept && raised_[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (kept && set == cudaSuccess) raised_[dev].store(true, std::memory_order_relaxed);
+    return set;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<bool> raised_[kDevices] = {};
+};
 
 enum { FP8_E4M3_CODES = 0, FP8_E5M2_CODES = 1 };
 

@@ -525,8 +525,8 @@ int long_blocks(int64_t cols) { return 4 * cols * 6 <= kRingBytes / 2 ? 2 : 1; }
 template <int R>
 cudaError_t run_long(const NormBwdArgs& p, int parts, unsigned* error, cudaStream_t st) {
   auto kernel = rmsnorm_backward_long_kernel<R>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes + 256);
+  static SmemLimit limit;
+  const cudaError_t attr = limit.raise(kernel, (int)kRingBytes + 256);
   if (attr != cudaSuccess) return attr;
   const int64_t slot = (int64_t)p.cols * 2 * (p.dres != nullptr ? 3 : 2);
   const int rows = (int)std::min<int64_t>(16, kRingBytes / long_blocks(p.cols) / slot);

@@ -274,3 +274,21 @@ def test_binding_refusals():
         fp.fp4_fp8_quantize(x[:0])
     with pytest.raises(KeyError):
         fp.fp4_fp8_quantize(x, "e3m4")
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_another_device_than_the_current_one():
+    """Each device runs every kernel on its own: what was set up for the first is not taken for the second."""
+    def run(dev):
+        g = torch.Generator().manual_seed(1)
+        out = []
+        for M, N, K in ((1, 256, 512), (100, 256, 512), (400, 512, 2048)):
+            a, b = (torch.randn(n, K, generator=g).to(torch.bfloat16).to(dev) for n in (M, N))
+            w = torch.ones(K, device=dev)
+            q, wq = fp.fp4_rmsnorm_fp8_quantize(a, w, a, sf_layout="mma"), fp.fp4_fp8_quantize(b, sf_layout="mma")
+            out += [fp.fp4_fp8_gemm(q.codes, q.scales, wq.codes, wq.scales),
+                    *fp.fp4_rmsnorm_backward(a, q.residual_out, w, q.rstd, a)]
+        torch.cuda.synchronize(dev)
+        return [t.cpu() for t in out]
+
+    assert all(torch.equal(a, b) for a, b in zip(run("cuda:0"), run("cuda:1")))
