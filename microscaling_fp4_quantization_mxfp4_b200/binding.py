@@ -27,7 +27,8 @@ _OUT = {"f32": OUT_F32, "bf16": OUT_BF16, torch.float32: OUT_F32, torch.bfloat16
         OUT_F32: OUT_F32, OUT_BF16: OUT_BF16}
 E4M3, E5M2 = 0, 1
 _FMT8 = {"e4m3": E4M3, "e5m2": E5M2, torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2, E4M3: E4M3, E5M2: E5M2}
-_BYTE = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu)
+_CODE8 = ((torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e5m2))      # by format
+_SCALE8 = (torch.uint8, torch.float8_e8m0fnu)
 FP8_BLOCK = 128
 BLOCK = {MXFP4: 32, NVFP4: 16, NVFP4_4O6: 16, MXFP4_GS: 32}
 
@@ -328,11 +329,11 @@ def _bf16_rows(t: torch.Tensor, dev: int, shape, name: str) -> int:
     return t.stride(0) if shape[0] != 1 else shape[1]
 
 
-def _codes8(t: torch.Tensor, dev: int, name: str, shape=None) -> int:
-    """Row stride of 8-bit codes (a single row: its length rounded up to 16)."""
-    if t.get_device() != dev or t.dtype not in _BYTE or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1) or \
+def _codes8(t: torch.Tensor, dev: int, fmt: int, name: str, shape=None) -> int:
+    """Row stride of 8-bit codes, bytes or the format's own type (a single row: its length rounded up to 16)."""
+    if t.get_device() != dev or t.dtype not in _CODE8[fmt] or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1) or \
             (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be a matrix of 8-bit codes" +
+        raise ValueError(f"{name} must be a matrix of {_CODE8[fmt][1]} codes or bytes" +
                          (f" of shape {tuple(shape)}" if shape is not None else "") + f" with unit column stride on cuda:{dev}")
     rows, cols = t.shape
     return t.stride(0) if rows != 1 else (cols + 15) // 16 * 16
@@ -346,12 +347,12 @@ def _scales_shape(rows: int, length: int, sf: int):
 def _scales8(t: torch.Tensor, dev: int, rows: int, length: int, sf: int, name: str) -> int:
     """Address of checked scale bytes."""
     shape = _scales_shape(rows, length, sf)
-    if t.get_device() != dev or t.dtype not in _BYTE or t.shape != shape or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype not in _SCALE8 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous scale bytes of shape {shape} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _fp8_outputs(x, dev, rows, length, sf, codes, scales, name=""):
+def _fp8_outputs(x, dev, rows, length, f, sf, codes, scales, name=""):
     """Checked or new codes [rows, length] and scales: (codes, row stride, scales).  New rows that are not whole
     16-byte pieces are padded to 128 bytes: the product reads 128-byte pieces of them, and rows 16 bytes off
     the next line cost it a fifth of its rate."""
@@ -362,7 +363,7 @@ def _fp8_outputs(x, dev, rows, length, sf, codes, scales, name=""):
             pitch = (length + 127) // 128 * 128
             codes = x.new_empty((rows, pitch), dtype=_u8)[:, :length]
     else:
-        pitch = _codes8(codes, dev, "codes" + name, (rows, length))
+        pitch = _codes8(codes, dev, f, "codes" + name, (rows, length))
     if scales is None:
         scales = x.new_empty(_scales_shape(rows, length, sf), dtype=_u8)
     else:
@@ -387,7 +388,7 @@ def fp4_fp8_quantize(x: torch.Tensor, fmt="e4m3", axis: int = 1, sf_layout="rowm
     f, sf = _FMT8[fmt], _SF[sf_layout]
     rows, cols = x.shape
     orows, length = (rows, cols) if axis == 1 else (cols, rows)
-    codes, pitch, scales = _fp8_outputs(x, dev, orows, length, sf, codes, scales)
+    codes, pitch, scales = _fp8_outputs(x, dev, orows, length, f, sf, codes, scales)
     _check(_lib.load().fp4_fp8_quantize(x.data_ptr(), rows, cols, x.stride(0) if rows != 1 else cols, f, axis,
                                         codes.data_ptr(), pitch, scales.data_ptr(), sf, _raw_stream(dev)),
            "fp4_fp8_quantize")
@@ -405,12 +406,12 @@ def fp4_fp8_quantize_2d(x: torch.Tensor, fmt="e4m3", sf_layout="rowmajor", trans
     _bf16_matrix(x)
     f, sf = _FMT8[fmt], _SF[sf_layout]
     rows, cols = x.shape
-    codes, pitch, scales = _fp8_outputs(x, dev, rows, cols, sf, codes, scales)
+    codes, pitch, scales = _fp8_outputs(x, dev, rows, cols, f, sf, codes, scales)
     pitch_t = 0
     if transposed:
-        codes_t, pitch_t, scales_t = _fp8_outputs(x, dev, cols, rows, sf, codes_t, scales_t, "_t")
-    else:
-        codes_t = scales_t = None
+        codes_t, pitch_t, scales_t = _fp8_outputs(x, dev, cols, rows, f, sf, codes_t, scales_t, "_t")
+    elif codes_t is not None or scales_t is not None:
+        raise ValueError("codes_t or scales_t is given without transposed")
     _check(_lib.load().fp4_fp8_quantize_2d(x.data_ptr(), rows, cols, x.stride(0) if rows != 1 else cols, f,
                                            codes.data_ptr(), pitch, scales.data_ptr(), _ptr(codes_t), pitch_t,
                                            _ptr(scales_t), sf, _raw_stream(dev)), "fp4_fp8_quantize_2d")
@@ -424,7 +425,7 @@ def fp4_fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, fmt="e4m3", sf
     if stream is not None or dev < 0 or dev != _device():
         return _elsewhere(fp4_fp8_dequantize, codes, stream, scales, fmt, sf_layout, out_dtype, out=out)
     f, sf, od = _FMT8[fmt], _SF[sf_layout], _OUT[out_dtype]
-    pitch = _codes8(codes, dev, "codes")
+    pitch = _codes8(codes, dev, f, "codes")
     rows, cols = codes.shape
     sptr = _scales8(scales, dev, rows, cols, sf, "scales")
     dtype = _f32 if od == OUT_F32 else _bf16
@@ -445,7 +446,7 @@ def fp4_fp8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.T
     if stream is not None or dev < 0 or dev != _device():
         return _elsewhere(fp4_fp8_gemm, a_codes, stream, a_scales, b_codes, b_scales, a_fmt, b_fmt, out_dtype, out=out)
     af, bf = _FMT8[a_fmt], _FMT8[b_fmt]
-    lda, ldb = _codes8(a_codes, dev, "a_codes"), _codes8(b_codes, dev, "b_codes")
+    lda, ldb = _codes8(a_codes, dev, af, "a_codes"), _codes8(b_codes, dev, bf, "b_codes")
     M, K = a_codes.shape
     N, kb = b_codes.shape
     if kb != K:
@@ -502,7 +503,7 @@ def fp4_rmsnorm_fp8_quantize(x: torch.Tensor, weight: torch.Tensor, residual: Op
         _fits(rstd, dev, _f32, (rows,), "rstd")
     if norm_out is not None:
         yptr = _fits(norm_out, dev, _bf16, shape, "norm_out").data_ptr()
-    codes, pitch, scales = _fp8_outputs(x, dev, rows, cols, sf, codes, scales)
+    codes, pitch, scales = _fp8_outputs(x, dev, rows, cols, f, sf, codes, scales)
     _check(_lib.load().fp4_rmsnorm_fp8_quantize(
         x.data_ptr(), x.stride(0) if rows != 1 else cols, rptr, ldr, weight.data_ptr(), wd, rows, cols, eps, f,
         codes.data_ptr(), pitch, scales.data_ptr(), sf, hptr, rstd.data_ptr(), yptr, _raw_stream(dev)),

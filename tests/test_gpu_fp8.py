@@ -276,6 +276,46 @@ def test_binding_refusals():
         fp.fp4_fp8_quantize(x, "e3m4")
 
 
+def test_types_of_codes_and_scales():
+    """Codes may have their format's own type, scales E8M0's; another format's type is refused, not read as this one's."""
+    x = torch.randn(4, 128, device="cuda", dtype=torch.bfloat16)
+    q = fp.fp4_fp8_quantize(x, "e5m2", sf_layout="mma")
+    c, s = q.codes.view(torch.float8_e5m2), q.scales.view(torch.float8_e8m0fnu)
+    assert torch.equal(fp.fp4_fp8_gemm(c, s, c, s, "e5m2", "e5m2"),
+                       fp.fp4_fp8_gemm(q.codes, q.scales, q.codes, q.scales, "e5m2", "e5m2"))
+    assert torch.equal(fp.fp4_fp8_dequantize(c, s, "e5m2", "mma"), fp.fp4_fp8_dequantize(q.codes, q.scales, "e5m2", "mma"))
+    for call in (lambda: fp.fp4_fp8_gemm(c, s, c, s), lambda: fp.fp4_fp8_gemm(c, s, c, s, "e5m2"),
+                 lambda: fp.fp4_fp8_dequantize(c, s, sf_layout="mma"), lambda: fp.fp4_fp8_quantize(x, codes=c),
+                 lambda: fp.fp4_fp8_dequantize(c, q.scales.view(torch.float8_e5m2), "e5m2", "mma"),
+                 lambda: fp.fp4_fp8_quantize_2d(x, transposed=False, codes_t=q.codes)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.parametrize("M, N, K", [(3, 40, 130), (100, 130, 300), (300, 260, 31), (600, 520, 2200)])
+def test_gemm_reads_nothing_past_its_operands(M, N, K):
+    """NaN codes past K in the rows, and NaN scales in the layout's padding, change no bit of the product."""
+    def operand(rows, seed):
+        g = torch.Generator().manual_seed(seed)
+        L = (K + 7) // 8 * 8
+        x = torch.randn(rows, L, generator=g).to(torch.bfloat16).cuda()
+        q = fp.fp4_fp8_quantize(x, sf_layout="mma")
+        wide = torch.full((rows, (K + 15) // 16 * 16 + 32), 0x7F, dtype=torch.uint8, device="cuda")
+        wide[:, :K] = q.codes[:, :K]
+        groups = (K + 127) // 128
+        byte = np.full(((rows + 127) // 128 * 128, (groups + 3) // 4 * 4), 255, np.uint8)
+        scales = fp.fp4_fp8_quantize(x).scales.cpu().numpy()[:, :groups]
+        byte[:rows, :groups] = scales
+        plain = np.zeros_like(byte)
+        plain[:rows, :groups] = scales
+        return (q.codes[:, :K], torch.from_numpy(fp8.mma(plain)).cuda(), wide[:, :K], torch.from_numpy(fp8.mma(byte)).cuda())
+
+    a, b = operand(M, 1), operand(N, 2)
+    want = fp.fp4_fp8_gemm(a[0], a[1], b[0], b[1], out_dtype="f32")
+    assert torch.all(torch.isfinite(want))
+    assert torch.equal(fp.fp4_fp8_gemm(a[2], a[3], b[2], b[3], out_dtype="f32"), want)
+
+
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
 def test_another_device_than_the_current_one():
     """Each device runs every kernel on its own: what was set up for the first is not taken for the second."""
