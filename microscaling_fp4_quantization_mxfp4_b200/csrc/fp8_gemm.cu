@@ -892,9 +892,9 @@ cudaError_t run_pairs(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
 
 template <bool BF16>
 cudaError_t dispatch(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
-  // Up to 128 rows of A: tiles of Y^T stream B over every SM (128 x 4096 x 4096: 10.1 against 12.8 us), unless more than
-  // half of them would be there for more than 64 rows (128 x 11008 x 4096: 15.5 against 14.6 us).
-  if (q.M > 128 || (q.M > 64 && 2 * ((q.N + 127) / 128) > num_sms)) {
+  // Up to 128 rows of A: tiles of Y^T stream B over every SM (128 x 4096 x 4096: 10.1 against 12.8 us in SM pairs;
+  // 128 x 11008 x 4096: 13.8 against 14.6; 128 x 32000 x 4096: 31.1 against 31.6).
+  if (q.M > 128) {
     const int64_t num_m = (q.M + 255) / 256, narrow = num_m * ((q.N + 191) / 192), wide = num_m * ((q.N + 255) / 256);
     const int64_t pairs = num_sms / 2, narrow_waves = (narrow + pairs - 1) / pairs, wide_waves = (wide + pairs - 1) / pairs;
     // Few tiles and a long K: K divided over clusters (256 x 1024 x 8192, 6 tiles: 12.7 against 19.1 us; 512 x 1024 x
