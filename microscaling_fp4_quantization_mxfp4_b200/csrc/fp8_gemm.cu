@@ -76,13 +76,15 @@ __device__ __forceinline__ void fp8_mma(uint32_t d, uint64_t adesc, uint64_t bde
 // ------------------------------------------------- tiles of Y^T over clusters --
 // Y^T = B . A^T in tiles of 128 rows of B by BNT rows of A (16 to 256), so that a product with few
 // activation rows fills the MMA's 128 rows with weights and reads each of them once.  A tile's blocks
-// of K are divided over a cluster of `split` CTAs; each CTA accumulates its share in tensor memory.  A
-// CTA on its own stores its tile from registers, 32 neighbours of a row of Y at a time (parking it first
-// in shared memory to store 16 bytes a thread was slower: 48 x 11008 x 4096 12.4 -> 11.5 us, 16 x 20000 x
-// 264 7.8 -> 6.6, 32 x 32000 x 4096 27.9 -> 26.3).  In a cluster the epilogue warps park it in the idle
-// stage ring (one row per row of A), and after a cluster barrier every CTA adds one slice over the
-// cluster through distributed shared memory, in rank order, and stores rows of Y.  Both cluster barriers
-// are reached on every path, errors included.
+// of K are divided over a cluster of `split` CTAs; each CTA accumulates its share in tensor memory.
+// A CTA on its own stores its tile from registers, 32 neighbours of a row of Y at a time (parking it first
+// in shared memory to store 16 bytes a thread was slower: 48 x 11008 x 4096 12.4 -> 11.5 us, 32 x 32000 x
+// 4096 27.9 -> 26.3).  In a cluster every CTA adds one slice of the tile, in rank order, and stores it.  Up
+// to 64 rows of A each CTA writes its share of a slice into the memory of the CTA that adds it, behind the
+// ring, and one cluster barrier later the sum reads its own memory.  More rows find no room there; their
+// shares are parked in the idle ring and read by the others between two barriers (for up to 64 rows that
+// took 7.0 against 6.5 us for 1 x 4096 x 4096, 8.7 against 8.1 for 64 x 4096 x 4096).  All barriers are
+// reached on every path, errors included.
 //
 // warp 0 TMA producer, warp 1 MMA issuer (one thread each), warps 2-5 epilogue, warp 6 scale copies.
 namespace tiles {
@@ -98,9 +100,14 @@ struct Cfg {
   static constexpr int kScaleBytes = (1 + kXAtoms) * 512;
   static constexpr int kStageBytes = kWBytes + kXBytes;
   static constexpr int kStages = std::min((kRing - (int)kScaleBufs * kScaleBytes) / kStageBytes, 12);
+  // Up to 64 rows of A, clusters have room behind fewer stages for the peers' shares of a CTA's own columns:
+  // [rank][row][slice_cols], where slice_cols * split is at most 144.
+  static constexpr bool kPush = BNT <= 64;
+  static constexpr int kRecvBytes = BNT * 144 * 4;
+  static constexpr int kPushStages = std::min((kRing - kRecvBytes - (int)kScaleBufs * kScaleBytes) / kStageBytes, 12);
   static constexpr int kPStride = 128 + 4;                       // floats of a parked row
   static constexpr int kRingBytes =
-      kStages * kStageBytes > BNT * kPStride * 4 ? kStages * kStageBytes : BNT * kPStride * 4;
+      std::max(kStages * kStageBytes, kPush ? kPushStages * kStageBytes + kRecvBytes : BNT * kPStride * 4);
   static constexpr int kSmem = 1024 + kRingBytes + (int)kScaleBufs * kScaleBytes + 512;
   static constexpr uint32_t kScaleCol = 256;                     // scale buffers after the accumulator
   static constexpr uint32_t kScaleCols = 16;                     // B's 4 columns, then A's 4 or 8
@@ -119,18 +126,71 @@ __device__ __forceinline__ void store_lane(const Fp8KernelArgs& p, const uint32_
   }
 }
 
-template <int BNT, bool BF16>
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Columns of a CTA's slice of the tile, a multiple of 4.
+__device__ __forceinline__ int slice_cols(int split) { return ((128 + split - 1) / split + 3) & ~3; }
+
+// NV rows from m0 on, in this lane's column: into the memory of the CTA that adds that column.
+template <int NV>
+__device__ __forceinline__ void push_lane(uint32_t dst, const uint32_t (&r)[NV], int m0, int rows, int slice) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (m0 + i >= rows) break;
+    st_cluster_u32(dst + (uint32_t)((m0 + i) * slice * 4), r[i]);
+  }
+}
+
+// Four neighbours of a row of Y from column n0 on.
+template <bool BF16>
+__device__ __forceinline__ void store4(const Fp8KernelArgs& p, const float4& v, int m, int n0) {
+  const float y4[4] = {v.x, v.y, v.z, v.w};
+  const long long o = (long long)m * p.ldy + n0;
+  if (BF16) {
+    __nv_bfloat16* yr = static_cast<__nv_bfloat16*>(p.y) + o;
+    if (p.vec_store && n0 + 4 <= p.N) {
+      *reinterpret_cast<uint2*>(yr) =
+          make_uint2((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[0])) |
+                         ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[1])) << 16),
+                     (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[2])) |
+                         ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[3])) << 16));
+    } else {
+      for (int i = 0; i < 4; ++i)
+        if (n0 + i < p.N) yr[i] = __float2bfloat16_rn(y4[i]);
+    }
+  } else {
+    float* yr = static_cast<float*>(p.y) + o;
+    if (p.vec_store && n0 + 4 <= p.N) {
+      *reinterpret_cast<float4*>(yr) = v;
+    } else {
+      for (int i = 0; i < 4; ++i)
+        if (n0 + i < p.N) yr[i] = y4[i];
+    }
+  }
+}
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
+  return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+
+template <int BNT, bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
     fp8_gemm_tile_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
-                         Fp8KernelArgs p, int split) {
+                         Fp8KernelArgs p, int cluster) {
   using C = Cfg<BNT>;
-  constexpr int S = C::kStages;
+  constexpr bool PUSH = CLUSTER && C::kPush;
+  constexpr int S = PUSH ? C::kPushStages : C::kStages;
+  const int split = CLUSTER ? cluster : 1;
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sW = smem;
   uint8_t* sX = sW + S * C::kWBytes;
   float* part = reinterpret_cast<float*>(smem);                  // reuses the ring after the last MMA
+  float* recv = reinterpret_cast<float*>(smem + C::kPushStages * C::kStageBytes);
   uint8_t* sScale = smem + C::kRingBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kScaleBufs * C::kScaleBytes);
   uint64_t* full = bars;
@@ -145,7 +205,7 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = split > 1 ? cluster_rank() : 0u;
+  const uint32_t rank = CLUSTER ? cluster_rank() : 0u;
   const int tile = (int)(blockIdx.x / (uint32_t)split);
   const int nt = tile % p.num_n, mt = tile / p.num_n;
   const int nkb = (p.K + kBK - 1) / kBK;
@@ -180,6 +240,7 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (PUSH) cluster_arrive();               // this CTA runs: its peers may write to its memory
   pdl_wait();                               // the previous kernel's outputs (our operands) are complete
 
   if (warp == 0) {
@@ -313,6 +374,7 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
     int ok = 1;
     if (lane == 0) ok = wait_bounded(smem_u32(tfull), 0u, abort_flag) ? 1 : 0;
     ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    if (PUSH) cluster_wait();               // the peers run
     if (!ok) {
       if (lane == 0) raise_abort(abort_flag, p.error);
     } else {
@@ -320,14 +382,20 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // ring bytes last touched by the async proxy
       float* col = part + q * 32 + lane;
+      const int n = q * 32 + lane, rows = p.M - mt * BNT, slice = slice_cols(split), owner = n / slice;
+      uint32_t dst = 0;
+      if (PUSH)
+        dst = map_rank(smem_u32(recv) + (uint32_t)(((int)rank * BNT * slice + n - owner * slice) * 4), (uint32_t)owner);
       if (BNT == 16) {
         uint32_t r[16];
         tmem_ld16(tbase, r);
         asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
                      "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
                      "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-        if (split == 1) {
-          store_lane<16, BF16>(p, r, mt * BNT, nt * 128 + q * 32 + lane);
+        if (!CLUSTER) {
+          store_lane<16, BF16>(p, r, mt * BNT, nt * 128 + n);
+        } else if (PUSH) {
+          push_lane<16>(dst, r, 0, rows, slice);
         } else {
 #pragma unroll
           for (int m = 0; m < 16; ++m) col[m * C::kPStride] = __uint_as_float(r[m]);
@@ -343,8 +411,10 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
                          "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
                          "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                          "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-          if (split == 1) {
-            store_lane<32, BF16>(p, r, mt * BNT + 32 * c, nt * 128 + q * 32 + lane);
+          if (!CLUSTER) {
+            store_lane<32, BF16>(p, r, mt * BNT + 32 * c, nt * 128 + n);
+          } else if (PUSH) {
+            push_lane<32>(dst, r, 32 * c, rows, slice);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) col[(32 * c + i) * C::kPStride] = __uint_as_float(r[i]);
@@ -353,12 +423,25 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
       }
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (split > 1) cluster_sync_all();        // every CTA's share is in its shared memory
-
   // ------------------------------------------- add one slice over the cluster --
-  if (split > 1) {
+  tc_fence_before();
+  if (PUSH) {
+    __syncwarp();
+    if (warp < 2 || warp == 6) cluster_wait();
+    cluster_sync_all();                     // every share of this CTA's columns is in its memory
+    const int slice = slice_cols(split), c0 = (int)rank * slice, rows = min(BNT, p.M - mt * BNT);
+    const int c4n = (min(min(128, p.N - nt * 128), c0 + slice) - c0 + 3) / 4;
+    const int across = slice / 4, c4 = (int)threadIdx.x % across, down = C::kThreads / across;
+    if (c4 < c4n && (int)threadIdx.x < down * across)
+      for (int r = (int)threadIdx.x / across; r < rows; r += down) {
+        const float* src = recv + r * slice + 4 * c4;
+        float4 acc = *reinterpret_cast<const float4*>(src);
+        for (int s = 1; s < split; ++s) acc = add4(acc, *reinterpret_cast<const float4*>(src + s * BNT * slice));
+        store4<BF16>(p, acc, mt * BNT + r, nt * 128 + c0 + 4 * c4);
+      }
+  } else if (CLUSTER) {
+    __syncthreads();
+    cluster_sync_all();                     // every CTA's share is in its shared memory
     const int rows = min(BNT, p.M - mt * BNT), nvalid = min(128, p.N - nt * 128);
     const int c4n = (nvalid + 3) / 4;                              // groups of four columns of Y
     const int items = rows * c4n;
@@ -374,39 +457,11 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
       float4 acc = v[0];
 #pragma unroll
       for (int s = 1; s < kMaxSplit; ++s)
-        if (s < split) {
-          acc.x = __fadd_rn(acc.x, v[s].x);
-          acc.y = __fadd_rn(acc.y, v[s].y);
-          acc.z = __fadd_rn(acc.z, v[s].z);
-          acc.w = __fadd_rn(acc.w, v[s].w);
-        }
-      const float y4[4] = {acc.x, acc.y, acc.z, acc.w};
-      const int n0 = nt * 128 + 4 * c4;
-      const long long o = (long long)(mt * BNT + r) * p.ldy + n0;
-      if (BF16) {
-        __nv_bfloat16* yr = static_cast<__nv_bfloat16*>(p.y) + o;
-        if (p.vec_store && n0 + 4 <= p.N) {
-          *reinterpret_cast<uint2*>(yr) =
-              make_uint2((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[0])) |
-                             ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[1])) << 16),
-                         (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[2])) |
-                             ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y4[3])) << 16));
-        } else {
-          for (int i = 0; i < 4; ++i)
-            if (n0 + i < p.N) yr[i] = __float2bfloat16_rn(y4[i]);
-        }
-      } else {
-        float* yr = static_cast<float*>(p.y) + o;
-        if (p.vec_store && n0 + 4 <= p.N) {
-          *reinterpret_cast<float4*>(yr) = acc;
-        } else {
-          for (int i = 0; i < 4; ++i)
-            if (n0 + i < p.N) yr[i] = y4[i];
-        }
-      }
+        if (s < split) acc = add4(acc, v[s]);
+      store4<BF16>(p, acc, mt * BNT + r, nt * 128 + 4 * c4);
     }
+    cluster_sync_all();                     // no CTA leaves while a peer may still read its share
   }
-  if (split > 1) cluster_sync_all();        // no CTA leaves while a peer may still read its share
   tc_fence_after();
   __syncthreads();
   if (warp == 1) {
@@ -815,7 +870,7 @@ int max_clusters(int split) {
   static int cache[tiles::kMaxSplit + 1] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (cache[split] == 0) {
-    auto kernel = tiles::fp8_gemm_tile_kernel<BNT, BF16>;
+    auto kernel = tiles::fp8_gemm_tile_kernel<BNT, BF16, true>;
     int n = 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split);
@@ -837,10 +892,11 @@ int max_clusters(int split) {
 template <int BNT, bool BF16>
 cudaError_t run_tiles(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
   using C = tiles::Cfg<BNT>;
-  static_assert(C::kStages >= 2 && C::kSmem <= 227 * 1024, "shared memory");
-  auto kernel = tiles::fp8_gemm_tile_kernel<BNT, BF16>;
-  static SmemLimit limit;
-  const cudaError_t attr = limit.raise(kernel, C::kSmem);
+  static_assert((C::kPush ? C::kPushStages : C::kStages) >= 2 && C::kSmem <= 227 * 1024, "shared memory");
+  auto alone = tiles::fp8_gemm_tile_kernel<BNT, BF16, false>, together = tiles::fp8_gemm_tile_kernel<BNT, BF16, true>;
+  static SmemLimit limit[2];
+  cudaError_t attr = limit[0].raise(alone, C::kSmem);
+  if (attr == cudaSuccess) attr = limit[1].raise(together, C::kSmem);
   if (attr != cudaSuccess) return attr;
   CUtensorMap tw, tx;
   if (!code_map(&tw, q.b, q.N, q.K, q.ldb, 128)) return cudaErrorNotSupported;
@@ -853,8 +909,8 @@ cudaError_t run_tiles(const Fp8GemmParams& q, int num_sms, cudaStream_t st) {
   // resident at once
   int64_t split = std::max<int64_t>(1, std::min<int64_t>({num_sms / n, (int64_t)tiles::kMaxSplit, nkb}));
   while (split > 1 && n > max_clusters<BNT, BF16>((int)split)) --split;
-  return launch_kernel(kernel, dim3((unsigned)(n * split)), dim3(C::kThreads), C::kSmem, st, false, (unsigned)split, tw,
-                       tx, p, (int)split);
+  return launch_kernel(split > 1 ? together : alone, dim3((unsigned)(n * split)), dim3(C::kThreads), C::kSmem, st, false,
+                       (unsigned)split, tw, tx, p, (int)split);
 }
 
 // Scales in the tensor-core layout as rows of 512 bytes (one 128 x 4 atom), one atom a box.

@@ -145,6 +145,13 @@ def test_gemm_lengths(K):
     _check_gemm(40, 200, K, seed=K)
 
 
+@pytest.mark.parametrize("M", [1, 20, 64, 65])
+@pytest.mark.parametrize("K", [256, 300, 500, 640, 700, 800, 1100])
+def test_gemm_slices(M, K):
+    """K over 2 to 8 CTAs: slices of 64 columns down to 16, those of 3, 5, 6 and 7 CTAs cut unevenly, on a short last tile."""
+    _check_gemm(M, 202, K, seed=9, ldy=203)
+
+
 @pytest.mark.parametrize("a_fmt, b_fmt", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2")])
 @pytest.mark.parametrize("M, N, K", [(1, 130, 300), (70, 260, 999), (600, 520, 1032)])
 def test_gemm_types(M, N, K, a_fmt, b_fmt):
