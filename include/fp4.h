@@ -399,8 +399,9 @@ fp4_status fp4_fp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_sf, cons
 /*
  * fp4_rmsnorm_fp8_quantize -- residual addition, RMS norm and FP8 quantization in one pass:
  *   h = bf16(x + residual), or x without one;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h * rstd * weight in
- *   fp32, quantized along the row as fp4_fp8_quantize does (axis 1).  Squares are fp32: a row whose |h| passes
- *   2^63 has rstd 0, and with eps = 0 one whose |h| stays below 2^-63 loses accuracy.
+ *   fp32, quantized along the row as fp4_fp8_quantize does (axis 1).  Mean and root are taken in 64 bits and rounded
+ *   to rstd once, whatever the row's magnitude; with eps = 0, rstd is infinite and the row NaN where the root mean
+ *   square is below 2^-128 (a row of zeros).
  *   x, residual    bf16 [rows, cols], row strides ldx and ldr (multiples of 8); residual nullable.
  *   weight         [cols], bf16 or fp32 (weight_dtype FP4_OUT_BF16 or FP4_OUT_F32).
  *   cols           a multiple of 8, at most 16384.

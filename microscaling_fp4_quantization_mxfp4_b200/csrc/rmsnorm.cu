@@ -8,7 +8,9 @@
 //   g = dy * weight, xh = h * rstd, c = mean(g * xh)
 //   dx = rstd * (g - xh * c) + dresidual,  dweight = sum over rows of dy * xh
 //
-// Sums and statistics are fp32 or wider (the rows' sums of squares and rstd in fp64, at no cost in time), y is fp32;
+// Sums and statistics are fp32 or wider, y is fp32.  The squares, their sum and its root are fp64, where no finite row
+// overflows or vanishes (a chunk's squares in fp32 made rows past 2^62.5 zero and rows near 1e-23 NaN, and took longer at
+// size: 16384 x 4096 76.1 against 73.0 us, 4096 x 11008 61.2 against 54.6; 300 x 4096 4.4 against 4.9);
 // the only roundings to fewer bits are the outputs' own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -80,11 +82,11 @@ struct NormArgs {
 
 // tpr threads a row, CPT 8-element chunks a thread: the row stays in registers between the sum of
 // squares and the quantization, so x and the residual are read once.  Bound by HBM (7 bytes an element
-// with a residual; 16384 x 4096: 76 us, 0.96 of the copy rate); one row of few: by the latency of load -> sum ->
+// with a residual; 16384 x 4096: 73 us, the copy rate); one row of few: by the latency of load -> sum ->
 // store (2.6 us).  Two chunks a thread took 91 us, eight 122: a row's fixed work (some 150 instructions a thread) is
 // spread over more elements, until the registers leave too few rows in flight.  Rows of up to 1024 elements are one
 // warp's, eight a block, and nothing waits for another warp.  MOST, BLOCKS: threads of a block, blocks an SM;
-// three blocks of up to 384 threads (56 registers) against two took 4096 x 11008 from 70.7 to 59.9 us.
+// three blocks of up to 384 threads (56 registers) against two took 4096 x 11008 from 70.7 to 59.9 us (54.6 now).
 constexpr int kShortThreads = 256;
 template <int FMT, int CPT, int MOST, int BLOCKS>
 __global__ void __launch_bounds__(MOST, BLOCKS) rmsnorm_fp8_kernel(NormArgs p) {
@@ -130,22 +132,20 @@ __global__ void __launch_bounds__(MOST, BLOCKS) rmsnorm_fp8_kernel(NormArgs p) {
       if (on[k]) *reinterpret_cast<uint4*>(out + k * TPR * 8) = h[k];
     }
   }
-  // a chunk's squares in fp32, the chunks' and threads' sums in fp64
-  double chunk_sums = 0.0;
+  // squares of bf16 are exact in fp64 and neither overflow nor vanish there
+  double sx = 0.0, sy = 0.0;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     float2 a[4];
     unpack2(h[k], a);
-    float2 s2 = fp4dev::mul2(a[0], a[0]);
 #pragma unroll
-    for (int i = 1; i < 4; ++i) s2 = __ffma2_rn(a[i], a[i], s2);
-    chunk_sums = __dadd_rn(chunk_sums, (double)__fadd_rn(s2.x, s2.y));
+    for (int i = 0; i < 4; ++i) {
+      sx = __fma_rn((double)a[i].x, (double)a[i].x, sx);
+      sy = __fma_rn((double)a[i].y, (double)a[i].y, sy);
+    }
   }
-  const double ss = row_sum64<WARP>(chunk_sums, part, slot * (TPR / 32), TPR / 32);
-  // 1 / sqrt(mean + eps), the fp32 root and one Newton step in fp64
-  const double ms = __fma_rn(ss, p.inv_cols, p.eps), r0 = (double)__frsqrt_rn((float)ms);
-  const double fix = __dmul_rn(__dmul_rn(0.5, r0), __fma_rn(-__dmul_rn(ms, r0), r0, 1.0));
-  const float rstd = (float)(isfinite(fix) ? __dadd_rn(r0, fix) : r0);
+  const double ss = row_sum64<WARP>(__dadd_rn(sx, sy), part, slot * (TPR / 32), TPR / 32);
+  const float rstd = (float)rsqrt(__fma_rn(ss, p.inv_cols, p.eps));
   if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
   const float2 r2 = make_float2(rstd, rstd);
   float2 y[CPT][4];

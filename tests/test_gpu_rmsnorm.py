@@ -272,3 +272,46 @@ def test_training_step(tokens):
     err = (cols + 16) * U * r64[:, None] * (g + xh * (g * xh).mean(axis=1, keepdims=True)) + 8 * U * np.abs(_f64(r))
     assert np.all(np.abs(_f64(dh) - want64) <= err + 2.0 ** -8 * (np.abs(want64) + err))
     assert np.all(np.abs(dw.double().cpu().numpy() - wantw) <= (tokens + 4) * U * (g * xh).sum(axis=0))
+
+
+def _check_rstd(rstd, want):
+    # the mean of squares and its root are taken in fp64 (squares of bf16 are exact there; 16384 additions are off by
+    # 2^-39 at most, in any order), so rstd is off by its rounding to fp32: U, or half the subnormals' step 2^-149
+    assert np.all(np.abs(rstd.double().cpu().numpy() - want) <= U * want * (1 + 2.0 ** -10) + 2.0 ** -150)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("cols", [8, 136, 1000, 2056, 4096, 11008, 16384])
+def test_norm_rstd_is_rounded_once(rows, cols):
+    x = _rand(rows, cols, rows * cols, 3.0)
+    eps = float(np.float32(1e-5))
+    q = fp.fp4_rmsnorm_fp8_quantize(x, torch.ones(cols, device="cuda"), eps=eps)
+    _check_rstd(q.rstd, fp8.rmsnorm(_f64(x), np.ones(cols), eps)[1])
+
+
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("cols", [8, 264, 2056, 4096])
+def test_norm_over_the_range_of_bf16(cols, few):
+    """Rows of any finite magnitude keep their values, with eps = 0 too: squares neither overflow nor vanish."""
+    g = torch.Generator().manual_seed(cols)
+    rows = [torch.full((cols,), 1.5 * 2.0 ** 62), torch.randn(cols, generator=g) * 1e37, torch.randn(cols, generator=g) * 1e-23,
+            torch.randn(cols, generator=g) * 1e-30, torch.full((cols,), 3.3e38), torch.full((cols,), 1e-37),
+            torch.randn(cols, generator=g), torch.where(torch.arange(cols) == cols - 3, 1.5 * 2.0 ** 63, 0.0),
+            torch.where(torch.arange(cols) % 8 < 3, 1e30, 1e-30), torch.where(torch.arange(cols) < 8, 1e-25, 0.0)]
+    x = torch.stack(rows).to(torch.bfloat16)
+    x = (x if few else x.repeat(30, 1)).cuda()
+    w = torch.ones(cols, device="cuda")
+    q = fp.fp4_rmsnorm_fp8_quantize(x, w, eps=0.0)
+    y, rstd = fp8.rmsnorm(_f64(x), np.ones(cols), 0.0)
+    _check_rstd(q.rstd, rstd)
+    # y: rstd's rounding (half the subnormals' step, 2^-150, of at least 2^-128: 2^-22) and two products, U each
+    _check_quantized(q.codes.cpu().numpy(), q.scales.cpu().numpy(), y, "e4m3", 2.0 ** -22 + 3 * U)
+
+
+def test_norm_past_the_range_of_rstd():
+    """eps = 0: rows whose root mean square is below 2^-128, zeros among them, have an infinite rstd and NaN codes."""
+    x = torch.zeros(3, 264, dtype=torch.bfloat16, device="cuda")
+    x[1], x[2] = 1e-40, 1.0
+    q = fp.fp4_rmsnorm_fp8_quantize(x, torch.ones(264, device="cuda"), eps=0.0)
+    assert torch.all(torch.isinf(q.rstd[:2])) and float(q.rstd[2]) == 1.0
+    assert torch.all(q.scales[:2] == 255) and torch.all(fp.fp4_fp8_dequantize(q.codes, q.scales)[2] == 1.0)
