@@ -59,8 +59,9 @@
  * 8-bit operators (fp4_fp8_*, fp4_rmsnorm_*), for the layers and gradients that four bits are too few
  * for:
  *  - Codes: one byte an element, E4M3 (largest value 448) or E5M2 (57344), rows `ldc` bytes apart
- *    (ldc >= L, a multiple of 16).  The bytes past L in a row are left as they are and may hold anything;
- *    operands are read in 16-byte pieces, so that every row's memory reaches to a multiple of 16.
+ *    (ldc >= L, a multiple of 16).  The bytes past L in a row are left as they are and may hold anything.
+ *    The product reads its operands in 16-byte pieces, so that every row's memory, the last one's too, reaches to
+ *    a multiple of 16; dequantization reads L bytes of each row.
  *  - Scales: one E8M0 byte b (2^(b-127)) per block of 128 elements along the row (the last block may be
  *    shorter) or per 128 x 128 tile, whose byte then stands in each of its rows.  The exponent is the
  *    least E >= -127 with amax <= Fmax * 2^E, so that no element saturates; byte 0 for an all-zero

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) fp8_quantize_tile_k
 }
 
 // ------------------------------------------------------------- dequantize --
-// One thread per 8 codes of a row: value = code * 2^(byte - 127) in fp32 (exact wherever the product
+// One thread per 8 codes of a row, nothing read past its end: value = code * 2^(byte - 127) in fp32 (exact wherever the product
 // is a normal fp32 number), rounded to bf16 on request.
 struct DeqArgs {
   const uint8_t* codes;
@@ -276,7 +276,14 @@ __global__ void __launch_bounds__(256) fp8_dequantize_kernel(DeqArgs p) {
     const uint32_t c = (uint32_t)(it - row * p.chunks) * 8;
     const uint32_t byte = p.scales[sf_offset(p.sf_mma, (long long)row, c >> 7, p.groups)];
     const float s = byte == kNanByte ? __uint_as_float(0x7FFFFFFFu) : fp4dev::mx_scale_value(byte);
-    const uint2 q = *reinterpret_cast<const uint2*>(p.codes + row * p.ldc + c);
+    const uint8_t* src = p.codes + row * p.ldc + c;
+    uint2 q = make_uint2(0, 0);
+    if (c + 8 <= p.cols) {
+      q = *reinterpret_cast<const uint2*>(src);
+    } else {                                  // a row's last codes: the bytes behind them need not be the caller's
+      for (int i = 0; i < 8; ++i)
+        if (c + i < p.cols) (i < 4 ? q.x : q.y) |= (uint32_t)src[i] << (8 * (i & 3));
+    }
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

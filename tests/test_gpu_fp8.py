@@ -339,3 +339,18 @@ def test_another_device_than_the_current_one():
         return [t.cpu() for t in out]
 
     assert all(torch.equal(a, b) for a, b in zip(run("cuda:0"), run("cuda:1")))
+
+
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("length", [1, 2, 3, 4, 5, 6, 7, 8, 9, 13, 127, 129, 1003])
+def test_dequantize_of_rows_that_end_with_their_codes(length, out_dtype):
+    """A row without padding, and a matrix whose last row ends with its last code."""
+    pitch = (length + 15) // 16 * 16
+    for rows in (1, 3):
+        g = np.random.default_rng(length + rows)
+        flat = g.integers(0, 256, ((rows - 1) * pitch + length,), dtype=np.uint8)
+        codes = torch.from_numpy(flat).cuda().as_strided((rows, length), (pitch if rows > 1 else length, 1))
+        byte = g.integers(100, 150, (rows, -(-length // 128)), dtype=np.uint8)
+        got = fp.fp4_fp8_dequantize(codes, torch.from_numpy(byte).cuda(), out_dtype=out_dtype)
+        want = torch.from_numpy(fp8.dequantize(codes.cpu().numpy(), byte)).float().to(got.dtype)
+        assert torch.equal(torch.nan_to_num(got.cpu(), 7.0), torch.nan_to_num(want, 7.0))
