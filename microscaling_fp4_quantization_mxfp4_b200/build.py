@@ -12,7 +12,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["api.cu", "quantize.cu", "mse.cu", "gemm.cu", "gemv.cu", "noalloc.cu", "fp8.cu", "fp8_gemm.cu", "rmsnorm.cu"]
-HEADERS = ["fp4_device.cuh", "fp4_internal.h", "fp8_device.cuh", "fp8_internal.h", "gemm_device.cuh"]
+HEADERS = ["copy_ring.h", "fp4_device.cuh", "fp4_internal.h", "fp8_device.cuh", "fp8_internal.h", "gemm_device.cuh"]
 LIB = os.path.join(PKG, "libfp4.so")
 OBJDIR = os.path.join(ROOT, "_build")
 

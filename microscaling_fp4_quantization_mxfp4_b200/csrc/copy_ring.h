@@ -1,0 +1,28 @@
+// Bookkeeping of a ring of shared-memory slots that asynchronous copies fill, each slot behind an mbarrier: when
+// the next copy may be asked for, and which copies may still be in flight once a wait has run out.  Plain integers,
+// so that it compiles for the host too, where a model of the barriers tests it.
+//
+// Copy n goes to slot n % slots and completes phase n / slots of the slot's barrier.  It is asked for only when copy
+// n - slots has landed and been read, so that at most one phase of a barrier is open.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define FP4_RING_FN __host__ __device__ __forceinline__
+#else
+#define FP4_RING_FN inline
+#endif
+
+namespace fp4ring {
+
+// A reader whose wait ran out (`late`) asks for no more: the slot's phase may still be open, and a second arrival
+// in it is undefined.
+FP4_RING_FN bool may_ask(bool late, uint32_t asked, uint32_t count) { return !late && asked < count; }
+
+// Of `asked` copies, those from this one on may be in flight.
+FP4_RING_FN uint32_t first_open(uint32_t asked, uint32_t slots) { return asked > slots ? asked - slots : 0u; }
+FP4_RING_FN uint32_t slot_of(uint32_t n, uint32_t slots) { return n % slots; }
+FP4_RING_FN uint32_t parity_of(uint32_t n, uint32_t slots) { return (n / slots) & 1u; }
+
+}  // namespace fp4ring

@@ -18,6 +18,7 @@
 
 #include <algorithm>
 
+#include "copy_ring.h"
 #include "fp4_device.cuh"
 #include "fp4_internal.h"
 #include "fp8_device.cuh"
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs
     if (++fetch_slot == ring_rows) fetch_slot = 0;
   };
   if (t == 0)
-    while (fetched < ring_rows && fetched < count) fetch();
+    while (fetched < ring_rows && fp4ring::may_ask(false, fetched, count)) fetch();
 #pragma unroll
   for (int k = 0; k < CPT; ++k)
     if (t + k * TPR < p.chunks) {
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs
       if (lane == 0) part[flip][r][warp] = sum[r];
     __syncthreads();                                           // one barrier for R rows: two sets of sums
     if (t == 0 && n0 > 0)
-      for (int r = 0; r < R && fetched < count; ++r) fetch();
+      for (int r = 0; r < R && fp4ring::may_ask(late, fetched, count); ++r) fetch();
 #pragma unroll
     for (int r = 0; r < R; ++r) sum[r] = lane < warps ? part[flip][r][lane] : 0.0f;
 #pragma unroll
@@ -466,8 +467,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_long_kernel(NormBwdArgs
     }
   }
   if (late && t == 0)                                          // no copy may land after the block has gone
-    for (int n = fetched > ring_rows ? fetched - ring_rows : 0; n < fetched; ++n)
-      fp4dev::mbar_wait_bounded(bar0 + 8 * (n % ring_rows), (uint32_t)(n / ring_rows) & 1u);
+    for (uint32_t n = fp4ring::first_open(fetched, ring_rows); n < (uint32_t)fetched; ++n)
+      fp4dev::mbar_wait_bounded(bar0 + 8 * fp4ring::slot_of(n, ring_rows), fp4ring::parity_of(n, ring_rows));
   store_partials<CPT>(p, acc, t, TPR);
 }
 
