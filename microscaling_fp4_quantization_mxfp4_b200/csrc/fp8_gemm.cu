@@ -128,9 +128,6 @@ __device__ __forceinline__ void store_lane(const Fp8KernelArgs& p, const uint32_
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 
 // Columns of a CTA's slice of the tile, a multiple of 4.
 __device__ __forceinline__ int slice_cols(int split) { return ((128 + split - 1) / split + 3) & ~3; }
@@ -597,6 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* sdrain = drain + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sdrain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  PairEnd* end = reinterpret_cast<PairEnd*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -622,6 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(drain), 1);
     mbar_init(smem_u32(sdrain), 1);
     *abort_flag = 0;
+    pair_end_init(end);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -644,7 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer --
     if (elect_one()) {
       int stage = 0;
-      uint32_t phase = 0, ns = 0;
+      uint32_t lap = 0, ns = 0;                                // rounds of the ring, scale copies asked for
       bool ok = true;
       for (int t = cluster; t < num_tiles && ok; t += nclusters) {
         int mt, nt;
@@ -652,7 +651,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < nkb; ++kb) {
           if ((kb & 3) == 0) {                                 // a new 512-element scale buffer
             const uint32_t b = ns % kScaleBufs, use = ns / kScaleBufs;
-            ++ns;
             if (!wait_spin(smem_u32(&sempty[b]), (use & 1u) ^ 1u, abort_flag)) {
               raise_abort(abort_flag, p.error);
               ok = false;
@@ -665,8 +663,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int atom = nt * TN / 128;                    // B's first atom (192: its rows may start in the middle)
             tma_load_2d_pair(dst + 512, &tmap_sb, 0, atom * p.g4 + (kb >> 2), lb);
             tma_load_2d_pair(dst + 1024, &tmap_sb, 0, (atom + 1) * p.g4 + (kb >> 2), lb);
+            ++ns;
           }
-          if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+          if (!wait_spin(smem_u32(&empty[stage]), (lap & 1u) ^ 1u, abort_flag)) {
             raise_abort(abort_flag, p.error);
             ok = false;
             break;
@@ -677,10 +676,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(smem_u32(sB + stage * C::kB), &tmap_b, kb * kBK, nt * TN + (int)rank * (TN / 2), fb);
           if (++stage == S) {
             stage = 0;
-            phase ^= 1u;
+            ++lap;
           }
         }
       }
+      pair_end_asked(end, rank, lap * S + (uint32_t)stage, ns);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -819,7 +819,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // an MMA warp that ends its tiles has seen every copy land; where a wait of the leader's ran out, those in
+  // flight are waited for
+  if (leader && threadIdx.x == 0 && *abort_flag != 0) pair_end_halt(end);
+  __syncwarp();
   cluster_sync_all();                  // neither CTA frees tensor memory or exits while the pair is busy
+  if (__builtin_expect(pair_halted(end), 0)) {
+    if (leader && threadIdx.x == 0 && settle_pair_copies(full, S, end, 0, C::kStageBytes))
+      settle_pair_copies(sload, kScaleBufs, end, 1, kScaleBytes);
+    __syncwarp();
+    cluster_sync_all();
+  }
   tc_fence_after();
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");

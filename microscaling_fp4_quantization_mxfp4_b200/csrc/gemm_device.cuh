@@ -9,6 +9,8 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include "copy_ring.h"
+
 namespace fp4tc {
 
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;   // 4 s per wait
@@ -224,6 +226,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Bytes announced on a barrier of this CTA that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
@@ -246,6 +255,43 @@ __device__ __forceinline__ void tc_commit_pair_local(uint32_t bar) {
 }
 __device__ __forceinline__ void tc_cp_sf_pair(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// How an SM pair ends: what its producers asked for, and whether a wait of the leader's ran out.
+// The leader's words are written by both CTAs before a cluster barrier and read behind it.
+struct PairEnd {
+  uint32_t halted;
+  uint32_t asked[2][2];            // [CTA][ring]: operands, scales
+};
+__device__ __forceinline__ void pair_end_init(PairEnd* e) {
+  volatile uint32_t* w = reinterpret_cast<volatile uint32_t*>(e);
+  for (int i = 0; i < 5; ++i) w[i] = 0u;
+}
+__device__ __forceinline__ void pair_end_asked(PairEnd* e, uint32_t rank, uint32_t operands, uint32_t scales) {
+  const uint32_t at = map_rank(smem_u32(&e->asked[rank][0]), 0);
+  st_cluster_u32(at, operands);
+  st_cluster_u32(at + 4u, scales);
+}
+__device__ __forceinline__ void pair_end_halt(PairEnd* e) {
+  for (uint32_t r = 0; r < 2; ++r) st_cluster_u32(map_rank(smem_u32(&e->halted), r), 1u);
+}
+__device__ __forceinline__ bool pair_halted(const PairEnd* e) { return *reinterpret_cast<const volatile uint32_t*>(&e->halted) != 0u; }
+
+// One thread of the leader, behind the cluster barrier that both producers have reached: waits (each wait bounded) for
+// the copies of ring `ring` that are still in flight.  `bytes`: one CTA's share of a copy.
+static __device__ __noinline__ bool settle_pair_copies(uint64_t* bars, uint32_t slots, const PairEnd* end, int ring,
+                                                       uint32_t bytes) {
+  struct {
+    uint32_t bar0, bytes;
+    __device__ void announce_one(uint32_t slot) { mbar_expect_tx(bar0 + 8u * slot, bytes); }
+    __device__ void forgo_one(uint32_t slot) { mbar_complete_tx(bar0 + 8u * slot, bytes); }
+    __device__ bool wait(uint32_t slot, uint32_t parity) {
+      volatile int never = 0;
+      return wait_bounded(bar0 + 8u * slot, parity, &never);
+    }
+  } barriers{smem_u32(bars), bytes};
+  const volatile uint32_t* asked = &end->asked[0][0];
+  return fp4ring::settle_pair(asked[ring], asked[2 + ring], slots, barriers);
 }
 
 // Called only between the two cluster barriers, which order it against the partials' stores.

@@ -95,4 +95,49 @@ int ring_faults(uint32_t slots, uint32_t count, uint32_t R, uint32_t stuck, uint
   return faults;
 }
 
+
+// An SM pair that stopped after `done` copies through the ring had landed and been read, `mine` asked for by the
+// leader and `peers` by its peer.  Bit n of own_late / peer_late: that CTA's share of copy done + n lands only while the
+// pair waits for it at the end.  Returns the faults, as above, and waits that run out.
+int pair_faults(uint32_t slots, uint32_t done, uint32_t mine, uint32_t peers, uint32_t own_late, uint32_t peer_late) {
+  struct Ring {
+    std::vector<Bar> bar;
+    struct Share {
+      uint32_t n;
+      bool landed;
+    };
+    std::vector<Share> shares;
+    uint32_t slots;
+    int faults = 0;
+    void announce_one(uint32_t slot) { bar[slot].announce(64); }
+    void forgo_one(uint32_t slot) { bar[slot].land(64); }
+    bool wait(uint32_t slot, uint32_t parity) {
+      for (Share& s : shares)
+        if (s.n % slots == slot && !s.landed) {
+          if (bar[slot].done(parity)) ++faults;           // the phase is over, a share of it still flies
+          s.landed = true;
+          bar[slot].land(64);
+        }
+      if (!bar[slot].done(parity)) ++faults;
+      return true;
+    }
+  } ring;
+  ring.bar.resize(slots);
+  ring.slots = slots;
+  for (uint32_t n = 0; n < (mine > peers ? mine : peers); ++n) {
+    const uint32_t slot = fp4ring::slot_of(n, slots);
+    if (n < mine) ring.bar[slot].announce(128);
+    for (int who = 0; who < 2; ++who) {
+      if (n >= (who ? peers : mine)) continue;
+      const bool late = n >= done && ((who ? peer_late : own_late) >> (n - done) & 1u);
+      ring.shares.push_back({n, !late});
+      if (!late) ring.bar[slot].land(64);
+    }
+  }
+  fp4ring::settle_pair(mine, peers, slots, ring);
+  for (const auto& s : ring.shares) ring.faults += s.landed ? 0 : 1;
+  for (const Bar& b : ring.bar) ring.faults += b.bad;
+  return ring.faults;
+}
+
 }

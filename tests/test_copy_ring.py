@@ -31,3 +31,16 @@ def test_a_late_reader_asks_for_no_more(model, rows_at_once):
                     assert model.ring_faults(*case, 0) == 0, case
                     caught += model.ring_faults(*case, 1) > 0
     assert caught                                       # the model sees the faults of a reader that goes on asking
+
+
+def test_a_pair_that_stops_waits_for_what_either_asked_for(model):
+    """Whatever each CTA of an SM pair has asked for, and whatever of it is in flight: all of it has landed at the end."""
+    for slots in (2, 3, 4, 7):
+        for done in (0, 1, slots, 2 * slots + 1):
+            for mine in range(done, done + slots + 1):
+                for peers in range(done, done + slots + 1):
+                    masks = range(1 << slots) if slots < 5 else (0, 1, 5, 64, 85, 127)
+                    for own in masks:
+                        for peer in masks:
+                            case = (slots, done, mine, peers, own, peer)
+                            assert model.pair_faults(*case) == 0, case
