@@ -250,7 +250,6 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
       for (int kb = kb0; kb < kb1; ++kb) {
         if (kb == kb0 || (kb & 3) == 0) {                        // a new 512-element scale buffer
           const uint32_t b = ns % kScaleBufs, use = ns / kScaleBufs;
-          ++ns;
           if (!wait_spin(smem_u32(&sempty[b]), (use & 1u) ^ 1u, abort_flag)) {
             raise_abort(abort_flag, p.error);
             ok = false;
@@ -263,6 +262,7 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
           for (int i = 0; i < x_atoms; ++i)
             bulk_load(smem_u32(dst + 512 * (1 + i)),
                       p.a_sf + ((size_t)(mt * C::kXAtoms + i) * p.g4 + (kb >> 2)) * 512, 512u, lb);
+          ++ns;
         }
         if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
           raise_abort(abort_flag, p.error);
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
         volatile int never = 0;
         for (int s = 0; s < S; ++s)
           if (issued & (1u << s)) wait_bounded(smem_u32(&full[s]), (issued_parity >> s) & 1u, &never);
-        for (uint32_t i = ns > kScaleBufs ? ns - kScaleBufs : 0; i < ns; ++i)
-          wait_bounded(smem_u32(&sload[i % kScaleBufs]), (i / kScaleBufs) & 1u, &never);
+        for (uint32_t i = fp4ring::first_open(ns, kScaleBufs); i < ns; ++i)
+          wait_bounded(smem_u32(&sload[fp4ring::slot_of(i, kScaleBufs)]), fp4ring::parity_of(i, kScaleBufs), &never);
       }
     }
     __syncwarp();

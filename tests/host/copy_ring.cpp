@@ -140,4 +140,28 @@ int pair_faults(uint32_t slots, uint32_t done, uint32_t mine, uint32_t peers, ui
   return ring.faults;
 }
 
+
+// A producer asked for `asked` copies, all but the last `slots` of which have landed, and waits at its end for those that
+// `counted` says may be in flight.  Returns those that still fly when it has gone.
+int copies_missed(uint32_t slots, uint32_t asked, uint32_t counted) {
+  std::vector<Bar> bar(slots);
+  std::vector<bool> flies(slots, false);
+  for (uint32_t n = 0; n < asked; ++n) {
+    const uint32_t s = fp4ring::slot_of(n, slots);
+    bar[s].announce(64);
+    if (n + slots < asked) bar[s].land(64);
+    else flies[s] = true;
+  }
+  for (uint32_t n = fp4ring::first_open(counted, slots); n < counted; ++n) {
+    const uint32_t s = fp4ring::slot_of(n, slots);
+    if (!bar[s].done(fp4ring::parity_of(n, slots)) && flies[s]) {         // it lands while it is waited for
+      flies[s] = false;
+      bar[s].land(64);
+    }
+  }
+  int missed = 0;
+  for (bool f : flies) missed += f;
+  return missed;
+}
+
 }

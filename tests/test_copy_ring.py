@@ -44,3 +44,12 @@ def test_a_pair_that_stops_waits_for_what_either_asked_for(model):
                         for peer in masks:
                             case = (slots, done, mine, peers, own, peer)
                             assert model.pair_faults(*case) == 0, case
+
+
+def test_a_producer_counts_the_copies_it_asked_for(model):
+    """One count too many, from before the wait that ran out, looks for a phase that never opens and misses the slot's own."""
+    for slots in (2, 4, 7):
+        for asked in range(1, 5 * slots):
+            assert model.copies_missed(slots, asked, asked) == 0
+            if asked >= slots:
+                assert model.copies_missed(slots, asked, asked + 1) == 1
