@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
   uint64_t* sdrain = tfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* asked = tmem_slot + 2;                      // copies of operands and of scales asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CLUSTER ? cluster_rank() : 0u;
@@ -245,14 +246,12 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
     if (elect_one()) {
       const int x_atoms = min(C::kXAtoms, (p.M + 127) / 128 - mt * C::kXAtoms);
       int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0, ns = 0;
-      bool ok = true;
+      uint32_t lap = 0, ns = 0;                                  // rounds of the ring, scale copies asked for
       for (int kb = kb0; kb < kb1; ++kb) {
         if (kb == kb0 || (kb & 3) == 0) {                        // a new 512-element scale buffer
           const uint32_t b = ns % kScaleBufs, use = ns / kScaleBufs;
           if (!wait_spin(smem_u32(&sempty[b]), (use & 1u) ^ 1u, abort_flag)) {
             raise_abort(abort_flag, p.error);
-            ok = false;
             break;
           }
           const uint32_t lb = smem_u32(&sload[b]);
@@ -264,30 +263,21 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
                       p.a_sf + ((size_t)(mt * C::kXAtoms + i) * p.g4 + (kb >> 2)) * 512, 512u, lb);
           ++ns;
         }
-        if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+        if (!wait_spin(smem_u32(&empty[stage]), (lap & 1u) ^ 1u, abort_flag)) {
           raise_abort(abort_flag, p.error);
-          ok = false;
           break;
         }
         const uint32_t fb = smem_u32(&full[stage]);
         mbar_expect_tx(fb, (uint32_t)C::kStageBytes);
         tma_load_2d(smem_u32(sW + stage * C::kWBytes), &tmap_w, kb * kBK, nt * 128, fb);
         tma_load_2d(smem_u32(sX + stage * C::kXBytes), &tmap_x, kb * kBK, mt * BNT, fb);
-        issued |= 1u << stage;
-        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == S) {
           stage = 0;
-          phase ^= 1u;
+          ++lap;
         }
       }
-      if (!ok) {
-        // let every copy already issued land before the CTA can exit
-        volatile int never = 0;
-        for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) wait_bounded(smem_u32(&full[s]), (issued_parity >> s) & 1u, &never);
-        for (uint32_t i = fp4ring::first_open(ns, kScaleBufs); i < ns; ++i)
-          wait_bounded(smem_u32(&sload[fp4ring::slot_of(i, kScaleBufs)]), fp4ring::parity_of(i, kScaleBufs), &never);
-      }
+      asked[0] = lap * S + (uint32_t)stage;
+      asked[1] = ns;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -461,6 +451,9 @@ __global__ void __launch_bounds__(Cfg<BNT>::kThreads, 1)
   }
   tc_fence_after();
   __syncthreads();
+  // where a wait ran out, its own or another warp's, the producer's copies still land before the CTA goes
+  if (__builtin_expect(*abort_flag != 0, 0) && threadIdx.x == 0 && settle_copies(full, S, asked[0]))
+    settle_copies(sload, kScaleBufs, asked[1]);
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
   }

@@ -294,6 +294,15 @@ static __device__ __noinline__ bool settle_pair_copies(uint64_t* bars, uint32_t 
   return fp4ring::settle_pair(asked[ring], asked[2 + ring], slots, barriers);
 }
 
+// One thread, behind the barrier that the producer has reached: waits (each wait bounded) for those of `asked` copies of
+// a ring that are still in flight.
+static __device__ __noinline__ bool settle_copies(uint64_t* bars, uint32_t slots, uint32_t asked) {
+  volatile int never = 0;
+  for (uint32_t n = fp4ring::first_open(asked, slots); n < asked; ++n)
+    if (!wait_bounded(smem_u32(&bars[fp4ring::slot_of(n, slots)]), fp4ring::parity_of(n, slots), &never)) return false;
+  return true;
+}
+
 // Called only between the two cluster barriers, which order it against the partials' stores.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
