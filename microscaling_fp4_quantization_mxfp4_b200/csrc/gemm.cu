@@ -643,6 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<BN, FMT>::kThre
   uint64_t* sf_empty = sf_full + kSfBufs;               // scale buffer b free (its MMAs done)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sf_empty + kSfBufs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  PairEnd* end = reinterpret_cast<PairEnd*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -663,6 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<BN, FMT>::kThre
       mbar_init(smem_u32(&sf_empty[b]), 1);
     }
     *abort_flag = 0;
+    pair_end_init(end);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -685,13 +687,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<BN, FMT>::kThre
     // ------------------------------------------------------------ producer --
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t lap = 0;                                 // rounds of the ring
       bool ok = true;
       for (int t = cluster; t < num_tiles && ok; t += nclusters) {
         int mt, nt;
         tile_coords(t, p.num_m, p.num_n, mt, nt);
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+          if (!wait_spin(smem_u32(&empty[stage]), (lap & 1u) ^ 1u, abort_flag)) {
             raise_abort(abort_flag, p.error);
             ok = false;
             break;
@@ -709,10 +711,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<BN, FMT>::kThre
                              (nt * C::kSfbBlocks + rb) * p.g4 + kb * APK, fb);
           if (++stage == S) {
             stage = 0;
-            phase ^= 1u;
+            ++lap;
           }
         }
       }
+      pair_end_asked(end, rank, lap * S + (uint32_t)stage, 0u);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -930,7 +933,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<BN, FMT>::kThre
   }
   tc_fence_before();
   __syncthreads();
+  // an MMA warp that ends its tiles has seen every copy land; where a wait of the leader's ran out, those in
+  // flight are waited for
+  if (leader && threadIdx.x == 0 && *abort_flag != 0) pair_end_halt(end);
+  __syncwarp();
   cluster_sync_all();                  // neither CTA frees tensor memory or exits while the pair is busy
+  if (__builtin_expect(pair_halted(end), 0)) {
+    if (leader && threadIdx.x == 0) settle_pair_copies(full, S, end, 0, C::kStageBytes);
+    __syncwarp();
+    cluster_sync_all();
+  }
   tc_fence_after();
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
