@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT>::kThreads, 1)
   uint64_t* sf_empty = sf_full + kSfBufs;               // scale buffer b free (its MMAs done)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sf_empty + kSfBufs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* asked = tmem_slot + 2;             // copies that the producer asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -268,8 +269,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT>::kThreads, 1)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
       int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued = 0, issued_parity = 0;   // per-stage bits: ever issued / parity of the last issue
+      uint32_t lap = 0;                         // rounds of the ring
       const int rb_total = (p.N + 127) / 128;
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT>::kThreads, 1)
         tile_coords(t, p.num_m, p.num_n, mt, nt);
         const int rb_here = min(BN / 128, rb_total - nt * (BN / 128));
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+          if (!wait_spin(smem_u32(&empty[stage]), (lap & 1u) ^ 1u, abort_flag)) {
             raise_abort(abort_flag, p.error);
             ok = false;
             break;
@@ -294,22 +294,13 @@ __global__ void __launch_bounds__(Cfg<BN, FMT>::kThreads, 1)
             bulk_load(smem_u32(sSFB + stage * C::kSfbBytes + rb * APK * 512),
                       p.b_sf + ((size_t)(nt * (BN / 128) + rb) * p.g4 + (size_t)kb * APK) * 512,
                       (uint32_t)atoms * 512u, fb);
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {
             stage = 0;
-            phase ^= 1u;
+            ++lap;
           }
         }
       }
-      if (!ok) {
-        // let every copy already issued land before the CTA can exit
-        for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) {
-            volatile int never = 0;
-            wait_bounded(smem_u32(&full[s]), (issued_parity >> s) & 1u, &never);
-          }
-      }
+      *asked = lap * S + (uint32_t)stage;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -548,6 +539,8 @@ __global__ void __launch_bounds__(Cfg<BN, FMT>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // where a wait ran out, its own or another warp's, the producer's copies still land before the CTA goes
+  if (threadIdx.x == 0 && __builtin_expect(*abort_flag != 0, 0)) settle_copies(full, S, *asked);
   tc_fence_after();
   if (warp == 1) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -998,6 +991,7 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
   uint64_t* sf_empty = sf_full + kSfBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sf_empty + kSfBufs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* asked = tmem_slot + 2;             // copies that the producer asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -1042,12 +1036,10 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
       const int rb_total = (p.N + 127) / 128;
       const int rb_here = min(BN / 128, rb_total - nt * (BN / 128));
       int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0;
-      bool ok = true;
+      uint32_t lap = 0;                         // rounds of the ring
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+        if (!wait_spin(smem_u32(&empty[stage]), (lap & 1u) ^ 1u, abort_flag)) {
           raise_abort(abort_flag, p.error);
-          ok = false;
           break;
         }
         const int kvalid = min(BK, p.K - kb * BK);
@@ -1062,20 +1054,12 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
           bulk_load(smem_u32(sSFB + stage * C::kSfbBytes + rb * APK * 512),
                     p.b_sf + ((size_t)(nt * (BN / 128) + rb) * p.g4 + (size_t)kb * APK) * 512, (uint32_t)atoms * 512u,
                     fb);
-        issued |= 1u << stage;
-        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == S) {
           stage = 0;
-          phase ^= 1u;
+          ++lap;
         }
       }
-      if (!ok) {
-        for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) {
-            volatile int never = 0;
-            wait_bounded(smem_u32(&full[s]), (issued_parity >> s) & 1u, &never);
-          }
-      }
+      *asked = lap * S + (uint32_t)stage;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -1192,6 +1176,9 @@ __global__ void __launch_bounds__(Cfg<BN, FMT, false>::kThreads, 1)
   (void)have_part;
   tc_fence_before();
   __syncthreads();
+  // where a wait ran out, its own or another warp's, the producer's copies still land before the CTA goes
+  if (threadIdx.x == 0 && __builtin_expect(*abort_flag != 0, 0)) settle_copies(full, S, *asked);
+  __syncwarp();
   cluster_sync_all();                 // every CTA's partial tile is in its shared memory
 
   // ------------------------------------------- reduce one slice across ranks --
@@ -1317,6 +1304,7 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
   uint64_t* sf_empty = sf_full + C::kSfBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sf_empty + C::kSfBufs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* asked = tmem_slot + 2;             // copies that the producer asked for
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = split > 1 ? cluster_rank() : 0u;
@@ -1358,12 +1346,10 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_w)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
       int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0;
-      bool ok = true;
+      uint32_t lap = 0;                         // rounds of the ring
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait_spin(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+        if (!wait_spin(smem_u32(&empty[stage]), (lap & 1u) ^ 1u, abort_flag)) {
           raise_abort(abort_flag, p.error);
-          ok = false;
           break;
         }
         const int kvalid = min(BK, p.K - kb * BK);
@@ -1375,20 +1361,12 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
         bulk_load(smem_u32(sSFW + stage * C::kSfBytes), p.b_sf + ((size_t)nt * p.g4 + (size_t)kb * APK) * 512,
                   (uint32_t)atoms * 512u, fb);
         bulk_load(smem_u32(sSFX + stage * C::kSfBytes), p.a_sf + (size_t)kb * APK * 512, (uint32_t)atoms * 512u, fb);
-        issued |= 1u << stage;
-        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == S) {
           stage = 0;
-          phase ^= 1u;
+          ++lap;
         }
       }
-      if (!ok) {
-        for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) {
-            volatile int never = 0;
-            wait_bounded(smem_u32(&full[s]), (issued_parity >> s) & 1u, &never);
-          }
-      }
+      *asked = lap * S + (uint32_t)stage;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -1515,6 +1493,9 @@ __global__ void __launch_bounds__(CfgS<BNT, FMT>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // where a wait ran out, its own or another warp's, the producer's copies still land before the CTA goes
+  if (threadIdx.x == 0 && __builtin_expect(*abort_flag != 0, 0)) settle_copies(full, S, *asked);
+  __syncwarp();
   if (split > 1) cluster_sync_all();  // every CTA's partial tile is in its shared memory
 
   // ------------------------------------------- reduce one slice across ranks --
