@@ -354,3 +354,30 @@ def test_dequantize_of_rows_that_end_with_their_codes(length, out_dtype):
         got = fp.fp4_fp8_dequantize(codes, torch.from_numpy(byte).cuda(), out_dtype=out_dtype)
         want = torch.from_numpy(fp8.dequantize(codes.cpu().numpy(), byte)).float().to(got.dtype)
         assert torch.equal(torch.nan_to_num(got.cpu(), 7.0), torch.nan_to_num(want, 7.0))
+
+
+def _operand_in_rows(rows, k, fmt, seed, pitch, tile=False):
+    """As _operand, rows `pitch` bytes apart and the values on the GPU."""
+    g = np.random.default_rng(seed)
+    codes, byte = fp8.quantize(g.standard_normal((rows, k)) * np.exp2(g.integers(-6, 7, (rows, 1))), fmt, tile)
+    c = torch.full((rows, pitch), 0x7F, dtype=torch.uint8)
+    c[:, :k] = torch.from_numpy(codes)
+    return c.cuda()[:, :k], torch.from_numpy(fp8.mma(byte)).cuda(), torch.from_numpy(fp8.dequantize(codes, byte, fmt)).cuda()
+
+
+@pytest.mark.parametrize("M, N, K, pitch, a_fmt, b_fmt", [
+    (4096, 4096, 2048, 2048, "e4m3", "e4m3"),      # 5 waves of 192 columns against 4 of 256, rows on sector borders
+    (4001, 4001, 2008, 2016, "e5m2", "e4m3"),      # the same, ragged
+    (2500, 5000, 1600, 1600, "e4m3", "e5m2"),      # 4 against 3
+    (4096, 5111, 520, 528, "e4m3", "e4m3")])       # 6 against 5 with a short K, rows off sector borders
+def test_gemm_waves_of_192_columns(M, N, K, pitch, a_fmt, b_fmt):
+    """The second accumulator and its reuse, with tiles whose scales start in the middle of an atom: every element."""
+    a, sa, av = _operand_in_rows(M, K, a_fmt, M + K, pitch)
+    b, sb, bv = _operand_in_rows(N, K, b_fmt, N + K, pitch, tile=True)
+    want, absum = av @ bv.t(), av.abs() @ bv.abs().t()
+    for dtype in (torch.float32, torch.bfloat16):
+        y = fp.fp4_fp8_gemm(a, sa, b, sb, a_fmt, b_fmt, out_dtype="f32" if dtype == torch.float32 else "bf16")
+        fp.fp4_check_device_errors()
+        assert y.dtype == dtype
+        tol = _bound(K, absum) + (0 if dtype == torch.float32 else 2.0 ** -8 * want.abs() * (1 + 2.0 ** -8))
+        assert bool(torch.all((y.double() - want).abs() <= tol))

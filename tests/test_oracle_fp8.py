@@ -85,3 +85,23 @@ def test_norm_gradient_against_differences(cols):
         d = np.zeros_like(w)
         d[j] = step
         assert abs((loss(h, w + d) - loss(h, w - d)) / (2 * step) - dw[j]) < 1e-7
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_non_finite_elements_reach_their_block_only(fmt, bad):
+    """Byte 255 and NaN codes in the element's whole 128 x 128 tile, or in its row's 1 x 128 block, and nowhere else."""
+    x = np.random.default_rng(10).standard_normal((150, 300))
+    x[3] = 0.0
+    x[5, 130], x[149, 0] = bad, bad
+    for tile in (True, False):
+        codes, byte = fp8.quantize(x, fmt, tile)
+        want = np.zeros(byte.shape, bool)
+        if tile:
+            want[:128, 1] = want[128:, 0] = True
+        else:
+            want[5, 1] = want[149, 0] = True
+            assert np.all(byte[3] == 0)
+        assert np.array_equal(byte == 255, want)
+        assert np.array_equal(np.isnan(fp8.decode(codes, fmt)), np.repeat(want, 128, axis=1)[:, :300])
+        assert np.array_equal(np.isnan(fp8.dequantize(codes, byte, fmt)), np.repeat(want, 128, axis=1)[:, :300])
