@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kRowThreads) fp8_quantize_rows_kernel(RowArgs 
     return;
   }
   const uint32_t lane = threadIdx.x & 31u, half = lane >> 4, c16 = lane & 15u;
-  const uint32_t warp = (blockIdx.x * kRowThreads + threadIdx.x) >> 5;
+  const uint32_t warp = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);       // threads may pass 32 bits, warps do not
   const uint32_t first = warp * (2 * kUnroll) + half;               // blocks first, first + 2, ... in row order
   uint4 v[kUnroll];
   uint32_t row[kUnroll], g[kUnroll];

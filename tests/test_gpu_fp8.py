@@ -381,3 +381,19 @@ def test_gemm_waves_of_192_columns(M, N, K, pitch, a_fmt, b_fmt):
         assert y.dtype == dtype
         tol = _bound(K, absum) + (0 if dtype == torch.float32 else 2.0 ** -8 * want.abs() * (1 + 2.0 ** -8))
         assert bool(torch.all((y.double() - want).abs() <= tol))
+
+
+def test_more_blocks_than_threads_in_32_bits():
+    """Past 2^30 blocks (rows of 8 elements) a thread's number passes 32 bits: the last rows are those of the same rows alone."""
+    rows, n = (1 << 30) + 1000, 2000
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    for part in (x[:n], x[-n:]):
+        part.copy_(torch.randn(n, 8, generator=g) * torch.exp2(torch.randint(-9, 9, (n, 1), generator=g).float()))
+    codes = torch.full((rows, 16), 0xA5, dtype=torch.uint8, device="cuda")[:, :8]
+    scales = torch.full((rows, 1), 0xA5, dtype=torch.uint8, device="cuda")
+    q = fp.fp4_fp8_quantize(x, codes=codes, scales=scales)
+    for part in (slice(0, n), slice(rows - n, rows)):
+        alone = fp.fp4_fp8_quantize(x[part].clone())
+        assert torch.equal(q.codes[part], alone.codes) and torch.equal(q.scales[part], alone.scales)
+    assert torch.all(q.codes[1 << 29:(1 << 29) + n] == 0) and torch.all(q.scales[1 << 29:(1 << 29) + n] == 0)
