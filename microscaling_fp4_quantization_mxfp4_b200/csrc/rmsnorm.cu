@@ -9,8 +9,10 @@
 //   dx = rstd * (g - xh * c) + dresidual,  dweight = sum over rows of dy * xh
 //
 // Sums and statistics are fp32 or wider, y is fp32.  The squares, their sum and its root are fp64, where no finite row
-// overflows or vanishes (a chunk's squares in fp32 made rows past 2^62.5 zero and rows near 1e-23 NaN, and took longer at
-// size: 16384 x 4096 76.1 against 73.0 us, 4096 x 11008 61.2 against 54.6; 300 x 4096 4.4 against 4.9);
+// overflows or vanishes.  Against eight squares at a time in fp32, which made rows past 2^62.5 zero and rows near 1e-23
+// NaN: 16384 x 4096 with a residual 75.3 -> 72.1 us, without one 45.7 -> 49.1; 4096 x 11008 60.2 -> 54.0; 50432 x 768
+// 47.6 -> 48.0; 300 x 4096 6.7 -> 7.1 (inputs past L2).  Squares of values moved to fp64 by integer arithmetic, in place of the
+// conversion, took longer (53.5 without a residual).
 // the only roundings to fewer bits are the outputs' own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -83,11 +85,11 @@ struct NormArgs {
 
 // tpr threads a row, CPT 8-element chunks a thread: the row stays in registers between the sum of
 // squares and the quantization, so x and the residual are read once.  Bound by HBM (7 bytes an element
-// with a residual; 16384 x 4096: 73 us, the copy rate); one row of few: by the latency of load -> sum ->
+// with a residual; 16384 x 4096: 72 us, the copy rate); one row of few: by the latency of load -> sum ->
 // store (2.6 us).  Two chunks a thread took 91 us, eight 122: a row's fixed work (some 150 instructions a thread) is
 // spread over more elements, until the registers leave too few rows in flight.  Rows of up to 1024 elements are one
 // warp's, eight a block, and nothing waits for another warp.  MOST, BLOCKS: threads of a block, blocks an SM;
-// three blocks of up to 384 threads (56 registers) against two took 4096 x 11008 from 70.7 to 59.9 us (54.6 now).
+// three blocks of up to 384 threads (56 registers) against two took 4096 x 11008 from 70.7 to 59.9 us (54.0 now).
 constexpr int kShortThreads = 256;
 template <int FMT, int CPT, int MOST, int BLOCKS>
 __global__ void __launch_bounds__(MOST, BLOCKS) rmsnorm_fp8_kernel(NormArgs p) {
@@ -134,18 +136,18 @@ __global__ void __launch_bounds__(MOST, BLOCKS) rmsnorm_fp8_kernel(NormArgs p) {
     }
   }
   // squares of bf16 are exact in fp64 and neither overflow nor vanish there
-  double sx = 0.0, sy = 0.0;
+  double sum = 0.0;
 #pragma unroll
   for (int k = 0; k < CPT; ++k) {
     float2 a[4];
     unpack2(h[k], a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sx = __fma_rn((double)a[i].x, (double)a[i].x, sx);
-      sy = __fma_rn((double)a[i].y, (double)a[i].y, sy);
+      sum = __fma_rn((double)a[i].x, (double)a[i].x, sum);
+      sum = __fma_rn((double)a[i].y, (double)a[i].y, sum);
     }
   }
-  const double ss = row_sum64<WARP>(__dadd_rn(sx, sy), part, slot * (TPR / 32), TPR / 32);
+  const double ss = row_sum64<WARP>(sum, part, slot * (TPR / 32), TPR / 32);
   const float rstd = (float)rsqrt(__fma_rn(ss, p.inv_cols, p.eps));
   if (live && t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
   const float2 r2 = make_float2(rstd, rstd);
