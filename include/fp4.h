@@ -390,7 +390,9 @@ fp4_status fp4_fp8_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* 
  *              independently.  16-byte aligned.
  *   a_sf, b_sf scales in FP4_SF_MMA layout, 16-byte aligned.
  *   y          fp32 or bf16 [M, N], row stride ldy >= N; aligned to its element.
- * M, N, K >= 1 arbitrary.  Forward: x and W; data gradient: dY and W^T of fp4_fp8_quantize_2d; weight
+ * M, N, K >= 1 arbitrary.  Products of codes are exact; the tensor cores' fp32 sums are within (K + 8) * 2^-23 *
+ * sum_k |a b| (measured: root mean square error 3.0e-7 of the result's at K = 8201 with fp32 output, where an fp32
+ * product of the same values has 1.0e-7).  Forward: x and W; data gradient: dY and W^T of fp4_fp8_quantize_2d; weight
  * gradient: dY and x both quantized along the tokens (axis 0).
  */
 fp4_status fp4_fp8_gemm(const uint8_t* a, int64_t lda, const uint8_t* a_sf, const uint8_t* b, int64_t ldb,

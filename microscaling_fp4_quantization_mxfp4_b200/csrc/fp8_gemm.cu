@@ -83,7 +83,7 @@ __device__ __forceinline__ void fp8_mma(uint32_t d, uint64_t adesc, uint64_t bde
 // to 64 rows of A each CTA writes its share of a slice into the memory of the CTA that adds it, behind the
 // ring, and one cluster barrier later the sum reads its own memory.  More rows find no room there; their
 // shares are parked in the idle ring and read by the others between two barriers (for up to 64 rows that
-// took 7.0 against 6.5 us for 1 x 4096 x 4096, 8.7 against 8.1 for 64 x 4096 x 4096).  All barriers are
+// took 7.0 against 6.6 us for 1 x 4096 x 4096, 8.7 against 7.9 for 64 x 4096 x 4096).  All barriers are
 // reached on every path, errors included.
 //
 // warp 0 TMA producer, warp 1 MMA issuer (one thread each), warps 2-5 epilogue, warp 6 scale copies.

@@ -13,7 +13,7 @@
 // NaN: 16384 x 4096 with a residual 75.3 -> 72.1 us, without one 45.7 -> 49.1; 4096 x 11008 60.2 -> 54.0; 50432 x 768
 // 47.6 -> 48.0; 300 x 4096 6.7 -> 7.1 (inputs past L2).  Squares of values moved to fp64 by integer arithmetic, in place of the
 // conversion, took longer (53.5 without a residual).
-// the only roundings to fewer bits are the outputs' own.
+// The only roundings to fewer bits are the outputs' own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
